@@ -413,6 +413,139 @@ int msa_sparse_attn_fused(msa_dtype dt, int B, int T, int T_loc, int Hq, int H, 
                           void* out, int32_t* mem_len, void* ws, size_t ws_bytes,
                           msa_stream_t stream);
 
+/* Per-head RMS norm of queries and keys with the position rotation, in one
+ * pass.  The Qwen3 backbone the pages name norms every query and key head
+ * before RoPE; [HYSEN] §"Document-wise RoPE ..." gives the rotation.  For
+ * each head row x of a token at position p:
+ *     y = R(p) (x * (mean(x^2) + eps)^(-1/2) * weight).
+ *   q            [n_tok] tokens of [Hq][D] (dt), q_stride elements from token
+ *                to token (>= Hq*D, a multiple of 16 bytes): a tensor of its
+ *                own or the slice of a fused projection's output.  Hq = 0:
+ *                none (q and q_out may be NULL).
+ *   k            the same with H heads and k_stride.  H = 0: none.
+ *   q_weight, k_weight  [D] (dt); NULL: that tensor is rotated only.
+ *   positions    [n_tok] int32 (device), any sign; NULL: normed only (as
+ *                msa_encode_pool wants its keys, which it rotates itself).
+ *   q_out, k_out [n_tok][Hq][D] and [n_tok][H][D] (dt), written.  An output
+ *                may be its own input where that is contiguous; it overlaps
+ *                nothing else.
+ * RoPE as in msa_encode_pool (pairs (i, i+D/2), base^(-2i/D)); angles are
+ * reduced exactly, for any int32 position.  Arithmetic in fp32, one rounding
+ * to dt.  n_tok = 0 does nothing.  Supported: D in {64,128}; any Hq, H up to
+ * 65536; n_tok < 2^31. */
+int msa_qk_norm_rope(msa_dtype dt, int64_t n_tok, int Hq, int H, int D, const void* q,
+                     int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                     const void* k_weight, const int32_t* positions, float eps,
+                     float rope_base, void* q_out, void* k_out, msa_stream_t stream);
+
+/* Backward of msa_qk_norm_rope, from the gradients of its outputs (the
+ * training step of msa_route_backward and msa_encode_pool_backward, carried
+ * on to the projections' outputs):
+ *     dz = R(-p) dy, r = (mean(x^2) + eps)^(-1/2), g = dz * weight,
+ *     dx = r (g - x r mean(g x r)), dweight = sum over rows of dz x r.
+ *   grad_dt       element type of dq_out, dk_out, dq and dk: MSA_F32 with any
+ *                 dt, or MSA_BF16 with MSA_BF16.
+ *   q, k, weights, positions, eps, rope_base: as in the forward call.
+ *   dq_out, dk_out  [n_tok][Hq][D], [n_tok][H][D] (grad_dt).
+ *   dq, dk        written, tokens dq_stride and dk_stride elements apart
+ *                 (>= heads*D, a multiple of 16 bytes); elements between the
+ *                 rows are left as they are.  May be dq_out / dk_out itself
+ *                 where that is contiguous.
+ *   dq_weight, dk_weight  [D] float, written (not accumulated); given
+ *                 exactly where the forward's weight was.
+ *   ws            >= msa_qk_norm_rope_backward_workspace_size() bytes, 16-byte
+ *                 aligned; unused (may be NULL) without weights.
+ * Sums in fp32, the weights' partial sums joined in double, in a fixed
+ * order: repeated calls give the same bits.  Otherwise as the forward. */
+size_t msa_qk_norm_rope_backward_workspace_size(int64_t n_tok, int D);
+int msa_qk_norm_rope_backward(msa_dtype dt, msa_dtype grad_dt, int64_t n_tok, int Hq, int H,
+                              int D, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* q_weight, const void* k_weight,
+                              const int32_t* positions, float eps, float rope_base,
+                              const void* dq_out, const void* dk_out, void* dq,
+                              int64_t dq_stride, void* dk, int64_t dk_stride,
+                              float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes,
+                              msa_stream_t stream);
+
+/* Append to a paged cache of the local context -- [HYSEN] §"Routing happens
+ * inside attention ..." (the query's local K/V grow by a token a step while
+ * it decodes) and §"Document-wise RoPE ..." (global positions, offset by k).
+ * The cache of one layer is a pool of pages; a sequence owns the pages its
+ * block-table row names, in order.
+ *   tok_offsets  [B+1] int64 (device): sequence b appends tokens
+ *                [tok_offsets[b], tok_offsets[b+1]) of the call; a sequence
+ *                may append none, and tokens before tok_offsets[0] or from
+ *                tok_offsets[B] on are padding: nothing is written for them,
+ *                queries included.
+ *   cache_len    [B] int32 (device): rows the sequence's cache holds; its
+ *                i-th appended token goes to row cache_len[b] + i.  The array
+ *                is not changed (drafted tokens may yet be rejected); the
+ *                caller advances it.
+ *   block_table  [B][max_pages] int32 (device): page of row r is
+ *                block_table[b][r / page_size].  Rows of two appended tokens
+ *                must not coincide (sequences share no page they write).
+ *   k_pages, v_pages [n_pages][H][page_size][D] (dt): a head's rows of a page
+ *                are contiguous.  Only the appended rows are written.
+ *   q, k, q_weight, k_weight, positions, eps, rope_base, q_out: as
+ *                msa_qk_norm_rope (positions required); the normed, rotated
+ *                keys go to the pages, the step's queries (Hq = 0: none) to
+ *                q_out in the same launch.
+ *   v            [n_tok] tokens of [H][D] (dt), v_stride apart; copied.
+ * A page id outside [0, n_pages) or a negative cache length records
+ * MSA_ERR_INVALID_ARG in the device status word, a row past the block table
+ * MSA_ERR_CAPACITY; that token's K and V are not written.
+ * Supported: page_size in {16,32,64,128}, D in {64,128},
+ * n_pages*H*page_size < 2^31. */
+int msa_paged_append(msa_dtype dt, int B, int64_t n_tok, int Hq, int H, int D, const void* q,
+                     int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const void* q_weight, const void* k_weight,
+                     const int64_t* tok_offsets, const int32_t* positions, float eps,
+                     float rope_base, const int32_t* block_table, int max_pages,
+                     const int32_t* cache_len, int page_size, int n_pages, void* k_pages,
+                     void* v_pages, void* q_out, msa_stream_t stream);
+
+/* Attention for trees of drafted tokens over [memory ; paged cache ; drafted
+ * tokens] -- [HYSEN] §"Routing happens inside attention ..." (the selected
+ * compressed K/V joined with the query's local K/V for autoregressive
+ * decoding), with the local context in a paged cache and one or more tokens
+ * a sequence to verify at once.  The drafted tokens have been appended
+ * (msa_paged_append) behind the cache_len[b] rows of their sequence.
+ *   q            [n_tok][Hq][D] (dt), already rotated; tok_offsets as in
+ *                msa_paged_append, at most n_max tokens a sequence.
+ *   parents      [n_tok] int32 (device): the parent of a token, as its index
+ *                within the sequence (smaller than the token's own), or -1
+ *                for a child of the last cached row.  NULL: a chain (each
+ *                token's parent is the one before it).  A value below -1
+ *                prunes the token and all below it: they see nothing and
+ *                their output is zero.
+ *   k_mem, v_mem [B][m_cap][H][D] (dt) with mem_len [B] int32 (device): as in
+ *                msa_sparse_attn; m_cap = 0: none (the three may be NULL).
+ *   k_pages, v_pages, block_table, cache_len: as in msa_paged_append.
+ *   out          [n_tok][Hq][D] (dt), written for the sequences' tokens only.
+ * Token i sees every memory row, every cached row, its ancestors and
+ * itself; keys and values it does not see (whatever they hold, NaN
+ * included) do not reach its output.  Query head h reads KV head
+ * floor(h*H/Hq).  scale <= 0 selects 1/sqrt(D).  Softmax and accumulation in
+ * fp32.
+ * Recorded in the device status word: MSA_ERR_INVALID_ARG for offsets
+ * outside [0, n_tok] or falling (the sequence is skipped), more than n_max
+ * tokens (only the first n_max are computed), a memory length outside
+ * [0, m_cap] (clamped), a negative cache length (taken as 0), a parent that
+ * is not before its token (pruned), a page id outside [0, n_pages) (the
+ * outputs of that sequence are unspecified); MSA_ERR_CAPACITY for more rows
+ * than the block table holds (rows past it are not seen).
+ * Supported: D in {64,128}, Hq % H == 0, Hq/H <= 16, 1 <= n_max <= 128,
+ * page_size in {16,32,64,128}, B*H <= 65535.  The workspace size is 0 for
+ * unsupported shapes and where none is needed. */
+size_t msa_tree_attn_workspace_size(msa_dtype dt, int B, int n_max, int Hq, int H, int D,
+                                    int m_cap, int max_pages, int page_size);
+int msa_tree_attn(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int D,
+                  const void* q, const int64_t* tok_offsets, const int32_t* parents,
+                  const void* k_mem, const void* v_mem, const int32_t* mem_len, int m_cap,
+                  const void* k_pages, const void* v_pages, int n_pages, int page_size,
+                  const int32_t* block_table, int max_pages, const int32_t* cache_len,
+                  float scale, void* out, void* ws, size_t ws_bytes, msa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

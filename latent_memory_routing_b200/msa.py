@@ -86,6 +86,18 @@ _SIGS = {
                                     c_p, c_sz, c_p]),
     "msa_sparse_attn": (c_i, [c_i, c_i, c_i, c_i, c_i, c_i, c_i, c_p, c_p, c_p, c_p, c_i, c_p,
                               c_p, c_i, c_f, c_f, c_p, c_p, c_sz, c_p]),
+    "msa_qk_norm_rope": (c_i, [c_i, c_i64, c_i, c_i, c_i, c_p, c_i64, c_p, c_i64, c_p, c_p, c_p,
+                               c_f, c_f, c_p, c_p, c_p]),
+    "msa_qk_norm_rope_backward_workspace_size": (c_sz, [c_i64, c_i]),
+    "msa_qk_norm_rope_backward": (c_i, [c_i, c_i, c_i64, c_i, c_i, c_i, c_p, c_i64, c_p, c_i64,
+                                        c_p, c_p, c_p, c_f, c_f, c_p, c_p, c_p, c_i64, c_p, c_i64,
+                                        c_p, c_p, c_p, c_sz, c_p]),
+    "msa_paged_append": (c_i, [c_i, c_i, c_i64, c_i, c_i, c_i, c_p, c_i64, c_p, c_i64, c_p, c_i64,
+                               c_p, c_p, c_p, c_p, c_f, c_f, c_p, c_i, c_p, c_i, c_i, c_p, c_p,
+                               c_p, c_p]),
+    "msa_tree_attn_workspace_size": (c_sz, [c_i] * 9),
+    "msa_tree_attn": (c_i, [c_i, c_i, c_i64, c_i, c_i, c_i, c_i, c_p, c_p, c_p, c_p, c_p, c_p, c_i,
+                            c_p, c_p, c_i, c_i, c_p, c_i, c_p, c_f, c_p, c_p, c_sz, c_p]),
 }
 
 
@@ -192,6 +204,30 @@ def _numel_ok(t, n, what, kind=None, host_ok=False):
             "the current CUDA device"
         raise ValueError(f"{what} is on {t.device}{' (pageable)' if not t.is_cuda else ''}; "
                          f"the kernels read it from {where}")
+
+
+def _rows_ok(t, n, heads, D, what, kind) -> int:
+    """Checks an operand of n tokens of [heads][D] whose tokens may lie apart
+    (a slice of a fused projection's output): each token's heads contiguous,
+    the tokens a fixed, 16-byte multiple of elements apart.  Returns that
+    stride (heads * D for a raw address, None or an empty tensor)."""
+    dense = heads * D
+    if t is None or isinstance(t, int):
+        return dense
+    want = _torch_dtype(kind)
+    if want is not None and t.dtype != want:
+        raise ValueError(f"{what} is {t.dtype}, the call reads {want}")
+    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, needs [>= {n}, {heads}, {D}]")
+    if t.shape[0] > 0 and heads > 0:
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+            raise ValueError(f"{what}: a token's heads must be contiguous")
+        if t.shape[0] > 1 and (t.stride(0) < dense or t.stride(0) * t.element_size() % 16):
+            raise ValueError(f"{what}: tokens must be a multiple of 16 bytes apart, and not "
+                             f"overlap (stride {t.stride(0)} elements)")
+    if not _device_ok(t, False):
+        raise ValueError(f"{what} is on {t.device}; it must be on the current CUDA device")
+    return t.stride(0) if t.shape[0] > 1 else dense
 
 
 def _ws_ok(ws, ws_bytes):
@@ -441,4 +477,97 @@ def msa_encode_pool_backward(L, n_tok, n_docs, H, D, dk_bar, dv_bar, dkr_bar, to
     _check("msa_encode_pool_backward", lib().msa_encode_pool_backward(
         L, n_tok, n_docs, H, D, _ptr(dk_bar), _ptr(dv_bar), _ptr(dkr_bar), _ptr(tok_offsets),
         _ptr(chunk_offsets), n_chunks, rope_base, _ptr(dk_tok), _ptr(dv_tok), _ptr(dkr_tok),
+        _stream(stream)))
+
+
+def msa_qk_norm_rope(dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base,
+                     q_out, k_out, stream=None):
+    """q and k: [n_tok][heads][D] tensors, the token strides taken from them
+    (raw addresses are dense)."""
+    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
+    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
+    _numel_ok(q_weight, D, "q_weight", _es(dt))
+    _numel_ok(k_weight, D, "k_weight", _es(dt))
+    _numel_ok(positions, n_tok, "positions", I32)
+    _numel_ok(q_out, n_tok * Hq * D, "q_out", _es(dt))
+    _numel_ok(k_out, n_tok * H * D, "k_out", _es(dt))
+    _check("msa_qk_norm_rope", lib().msa_qk_norm_rope(
+        dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+        _ptr(positions), eps, rope_base, _ptr(q_out), _ptr(k_out), _stream(stream)))
+
+
+def msa_qk_norm_rope_backward_workspace_size(n_tok, D) -> int:
+    return lib().msa_qk_norm_rope_backward_workspace_size(n_tok, D)
+
+
+def msa_qk_norm_rope_backward(dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions,
+                              eps, rope_base, dq_out, dk_out, dq, dk, dq_weight, dk_weight, ws,
+                              ws_bytes, stream=None):
+    """q, k, dq and dk: [n_tok][heads][D] tensors, the token strides taken
+    from them (raw addresses are dense)."""
+    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
+    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
+    dqs = _rows_ok(dq, n_tok, Hq, D, "dq", _es(grad_dt))
+    dks = _rows_ok(dk, n_tok, H, D, "dk", _es(grad_dt))
+    _numel_ok(q_weight, D, "q_weight", _es(dt))
+    _numel_ok(k_weight, D, "k_weight", _es(dt))
+    _numel_ok(positions, n_tok, "positions", I32)
+    _numel_ok(dq_out, n_tok * Hq * D, "dq_out", _es(grad_dt))
+    _numel_ok(dk_out, n_tok * H * D, "dk_out", _es(grad_dt))
+    _numel_ok(dq_weight, D, "dq_weight", F32)
+    _numel_ok(dk_weight, D, "dk_weight", F32)
+    _ws_ok(ws, ws_bytes)
+    _check("msa_qk_norm_rope_backward", lib().msa_qk_norm_rope_backward(
+        dt, grad_dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+        _ptr(positions), eps, rope_base, _ptr(dq_out), _ptr(dk_out), _ptr(dq), dqs, _ptr(dk), dks,
+        _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_offsets, positions,
+                     eps, rope_base, block_table, max_pages, cache_len, page_size, n_pages,
+                     k_pages, v_pages, q_out, stream=None):
+    """q, k and v: [n_tok][heads][D] tensors, the token strides taken from
+    them (raw addresses are dense)."""
+    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
+    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
+    vs = _rows_ok(v, n_tok, H, D, "v", _es(dt))
+    _numel_ok(q_weight, D, "q_weight", _es(dt))
+    _numel_ok(k_weight, D, "k_weight", _es(dt))
+    _numel_ok(tok_offsets, B + 1, "tok_offsets", I64)
+    _numel_ok(positions, n_tok, "positions", I32)
+    _numel_ok(block_table, B * max_pages, "block_table", I32)
+    _numel_ok(cache_len, B, "cache_len", I32)
+    _numel_ok(k_pages, n_pages * H * page_size * D, "k_pages", _es(dt))
+    _numel_ok(v_pages, n_pages * H * page_size * D, "v_pages", _es(dt))
+    _numel_ok(q_out, n_tok * Hq * D, "q_out", _es(dt))
+    _check("msa_paged_append", lib().msa_paged_append(
+        dt, B, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
+        _ptr(k_weight), _ptr(tok_offsets), _ptr(positions), eps, rope_base, _ptr(block_table),
+        max_pages, _ptr(cache_len), page_size, n_pages, _ptr(k_pages), _ptr(v_pages),
+        _ptr(q_out), _stream(stream)))
+
+
+def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size) -> int:
+    return lib().msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size)
+
+
+def msa_tree_attn(dt, B, n_tok, n_max, Hq, H, D, q, tok_offsets, parents, k_mem, v_mem, mem_len,
+                  m_cap, k_pages, v_pages, n_pages, page_size, block_table, max_pages, cache_len,
+                  scale, out, ws, ws_bytes, stream=None):
+    _numel_ok(q, n_tok * Hq * D, "q", _es(dt))
+    _numel_ok(tok_offsets, B + 1, "tok_offsets", I64)
+    _numel_ok(parents, n_tok, "parents", I32)
+    _numel_ok(k_mem, B * m_cap * H * D, "k_mem", _es(dt))
+    _numel_ok(v_mem, B * m_cap * H * D, "v_mem", _es(dt))
+    _numel_ok(mem_len, B if m_cap else 0, "mem_len", I32)
+    _numel_ok(k_pages, n_pages * H * page_size * D, "k_pages", _es(dt))
+    _numel_ok(v_pages, n_pages * H * page_size * D, "v_pages", _es(dt))
+    _numel_ok(block_table, B * max_pages, "block_table", I32)
+    _numel_ok(cache_len, B, "cache_len", I32)
+    _numel_ok(out, n_tok * Hq * D, "out", _es(dt))
+    _ws_ok(ws, ws_bytes)
+    _check("msa_tree_attn", lib().msa_tree_attn(
+        dt, B, n_tok, n_max, Hq, H, D, _ptr(q), _ptr(tok_offsets), _ptr(parents), _ptr(k_mem),
+        _ptr(v_mem), _ptr(mem_len), m_cap, _ptr(k_pages), _ptr(v_pages), n_pages, page_size,
+        _ptr(block_table), max_pages, _ptr(cache_len), scale, _ptr(out), _ptr(ws), ws_bytes,
         _stream(stream)))

@@ -6,6 +6,8 @@ into libmsa.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import msa as _m
@@ -319,6 +321,198 @@ class Pipeline:
         self.attn(q, self.k_mem, self.v_mem, self.mem_len, k_loc, v_loc, self.pos0,
                   self.rope_base, 0.0, self.out, stream)
         return self.out
+
+
+def _on(stream):
+    """Tensors made in this context belong to the stream the call runs on (an
+    int is a raw handle), so their memory is not handed on while it runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 rope_base: float = 10000.0, out=None, stream=None):
+    """Per-head RMS norm of q [N][Hq][D] and k [N][H][D] (either may be None)
+    with RoPE at ``positions`` [N] (int32) in the same pass.  A weight of None
+    leaves that tensor unnormed, ``positions`` of None unrotated.  The tokens
+    of q and k may lie apart (slices of a fused projection's output); the
+    outputs are contiguous.  ``out`` = (q_out, k_out) to reuse; returns them."""
+    x = q if q is not None else k
+    n, _, D = x.shape
+    Hq, H = (0 if t is None else t.shape[1] for t in (q, k))
+    if out is None:
+        with _on(stream):
+            out = tuple(None if t is None else torch.empty((n, t.shape[1], D), dtype=t.dtype,
+                                                           device=t.device) for t in (q, k))
+    _m.msa_qk_norm_rope(dt_code(x), n, Hq, H, D, q, k, q_weight, k_weight, positions, eps,
+                        rope_base, *out, stream)
+    return out
+
+
+def qk_norm_rope_backward_workspace(q, k):
+    """The workspace msa_qk_norm_rope_backward needs for these shapes (None
+    if none)."""
+    x = q if q is not None else k
+    n = _m.msa_qk_norm_rope_backward_workspace_size(x.shape[0], x.shape[2])
+    return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+
+
+def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weight=None,
+                          eps: float = 1e-6, rope_base: float = 10000.0, out=None, ws=None,
+                          stream=None):
+    """Gradients of qk_norm_rope's inputs from those of its outputs (fp32, or
+    bf16 with bf16 inputs): returns (dq, dk, dq_weight, dk_weight), the first
+    two in the gradients' type, the weights' in fp32 (None where the input is
+    None).  ``out``: the four to reuse (dq and dk may be slices, as q and k).
+    ``ws``: from qk_norm_rope_backward_workspace (made here if None)."""
+    x, dy = (q, dq_out) if q is not None else (k, dk_out)
+    n, _, D = x.shape
+    Hq, H = (0 if t is None else t.shape[1] for t in (q, k))
+    with _on(stream):
+        if ws is None:
+            ws = qk_norm_rope_backward_workspace(q, k)
+        if out is None:
+            out = tuple(None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                        for t in (dq_out, dk_out))
+            out += tuple(None if t is None or w is None else
+                         torch.empty(D, dtype=torch.float32, device=t.device)
+                         for t, w in ((q, q_weight), (k, k_weight)))
+    _m.msa_qk_norm_rope_backward(dt_code(x), dt_code(dy), n, Hq, H, D, q, k, q_weight, k_weight,
+                                 positions, eps, rope_base, dq_out, dk_out, *out, ws,
+                                 0 if ws is None else ws.numel(), stream)
+    return out
+
+
+class PagedCache:
+    """The local context of B sequences (one layer) in pages of
+    ``page_size`` rows: the pools k_pages, v_pages [n_pages][H][page_size][D],
+    the sequences' page lists block_table [B][max_pages] and their lengths
+    cache_len [B] (int32, device).  Pages are handed out on the host
+    (``reserve``, ``release``); rows are written by ``append``."""
+
+    def __init__(self, dtype, n_pages: int, page_size: int, H: int, D: int, B: int,
+                 max_pages: int, device):
+        self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
+        self.B, self.H, self.D = B, H, D
+        self.k_pages = torch.empty((n_pages, H, page_size, D), dtype=dtype, device=device)
+        self.v_pages = torch.empty_like(self.k_pages)
+        self.block_table = torch.zeros((B, max_pages), dtype=torch.int32, device=device)
+        self.cache_len = torch.zeros(B, dtype=torch.int32, device=device)
+        self.free = list(range(n_pages - 1, -1, -1))
+        self.owned = [[] for _ in range(B)]
+
+    def reserve(self, b: int, rows: int):
+        """Gives sequence b pages for at least ``rows`` rows in all."""
+        have = len(self.owned[b])
+        need = -(-rows // self.page_size) - have
+        if need <= 0:
+            return
+        if need > len(self.free) or have + need > self.max_pages:
+            raise _m.MsaError("PagedCache.reserve", -3, f"sequence {b}, {rows} rows")
+        new = [self.free.pop() for _ in range(need)]
+        self.owned[b] += new
+        self.block_table[b, have:have + need] = torch.tensor(
+            new, dtype=torch.int32, device=self.block_table.device)
+
+    def release(self, b: int):
+        """Takes sequence b's pages back and empties it."""
+        self.free += reversed(self.owned[b])
+        self.owned[b] = []
+        self.cache_len[b] = 0
+
+    def append(self, k, v, tok_offsets, positions, k_weight=None, q=None, q_weight=None,
+               eps: float = 1e-6, rope_base: float = 10000.0, q_out=None, stream=None):
+        """Writes the tokens' keys (normed where ``k_weight`` is given, and
+        rotated) and values behind the sequences' cached rows; cache_len is
+        left to the caller (``cache_len.add_(kept)``).  Given the step's
+        queries ``q`` [N][Hq][D], norms and rotates them in the same launch
+        and returns them (``q_out``, made here if None)."""
+        n = k.shape[0]
+        Hq = 0 if q is None else q.shape[1]
+        if q is not None and q_out is None:
+            with _on(stream):
+                q_out = torch.empty((n, Hq, self.D), dtype=q.dtype, device=q.device)
+        _m.msa_paged_append(dt_code(k), self.B, n, Hq, self.H, self.D, q, k, v, q_weight,
+                            k_weight, tok_offsets, positions, eps, rope_base, self.block_table,
+                            self.max_pages, self.cache_len, self.page_size, self.n_pages,
+                            self.k_pages, self.v_pages, q_out, stream)
+        return q_out
+
+
+class TreeAttention:
+    """Holds the workspace of msa_tree_attn for fixed shapes: up to ``n_max``
+    drafted tokens a sequence over [memory ; paged cache ; drafted tokens]."""
+
+    def __init__(self, dtype, B, n_max, Hq, H, D, m_cap, max_pages, page_size, device):
+        self.dt = _m.dtype_code(dtype)
+        self.shape = (B, n_max, Hq, H, D, m_cap)
+        n = _m.msa_tree_attn_workspace_size(self.dt, B, n_max, Hq, H, D, m_cap, max_pages,
+                                            page_size)
+        self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+    def __call__(self, q, tok_offsets, cache: PagedCache, parents=None, k_mem=None, v_mem=None,
+                 mem_len=None, scale: float = 0.0, out=None, stream=None):
+        B, n_max, Hq, H, D, m_cap = self.shape
+        if (cache.B, cache.H, cache.D) != (B, H, D):
+            raise ValueError(f"the cache holds {cache.B} x {cache.H} x {cache.D}, "
+                             f"the attention was made for {B} x {H} x {D}")
+        if out is None:
+            with _on(stream):
+                out = torch.empty_like(q)
+        _m.msa_tree_attn(self.dt, B, q.shape[0], n_max, Hq, H, D, q, tok_offsets, parents, k_mem,
+                         v_mem, mem_len, m_cap, cache.k_pages, cache.v_pages, cache.n_pages,
+                         cache.page_size, cache.block_table, cache.max_pages, cache.cache_len,
+                         scale, out, self.ws, self.ws.numel(), stream)
+        return out
+
+
+class CachedPipeline:
+    """Generation over a resident pooled bank with the local context in a
+    PagedCache (one layer): ``select`` routes the sequences' queries and
+    gathers their documents' memory, ``step`` appends a step's tokens (one a
+    sequence, a chain, or a drafted tree) and attends over [memory ; cache ;
+    tokens].  After a step the caller advances ``cache.cache_len`` by the rows
+    it keeps; to keep a path of a tree, it appends that path's tokens again
+    (same positions) and advances by their number."""
+
+    def __init__(self, kr_bar, k_bar, v_bar, chunk_offsets, cache: PagedCache, *, T, n_max, Hq, k,
+                 m_cap, rope_base=10000.0, eps=1e-6, prepared=False):
+        C, H, D = kr_bar.shape
+        dev, B = kr_bar.device, cache.B
+        self.kr_bar, self.k_bar, self.v_bar, self.coff = kr_bar, k_bar, v_bar, chunk_offsets
+        self.cache, self.m_cap, self.rope_base, self.eps = cache, m_cap, rope_base, eps
+        self.k, self.n_docs = k, chunk_offsets.numel() - 1
+        self.router = Router(kr_bar.dtype, B, T, H, D, dev, prepared=prepared)
+        self.attn = TreeAttention(kr_bar.dtype, B, n_max, Hq, H, D, m_cap, cache.max_pages,
+                                  cache.page_size, dev)
+        self.doc_scores = torch.empty((B, self.n_docs), dtype=torch.float32, device=dev)
+        self.idx = torch.empty((B, k), dtype=torch.int32, device=dev)
+        self.top = torch.empty((B, k), dtype=torch.float32, device=dev)
+        self.topk_ws = topk_workspace(B, self.n_docs, k, dev)
+        self.k_mem = torch.empty((B, m_cap, H, D), dtype=kr_bar.dtype, device=dev)
+        self.v_mem = torch.empty_like(self.k_mem)
+        self.mem_len = torch.zeros(B, dtype=torch.int32, device=dev)
+
+    def select(self, q_r, stream=None):
+        """Routes q_r [B][T][H][D]; the selected documents' rows become every
+        later step's memory.  Returns the selected documents [B][k]."""
+        self.router(q_r, self.kr_bar, self.coff, self.n_docs, self.doc_scores, None, stream)
+        topk_docs(self.doc_scores, self.k, self.idx, self.top, self.topk_ws, stream)
+        gather_kv(self.idx, self.coff, self.k_bar, self.v_bar, self.m_cap, self.k_mem,
+                  self.v_mem, self.mem_len, stream)
+        return self.idx
+
+    def step(self, q, k, v, tok_offsets, positions, parents=None, q_weight=None, k_weight=None,
+             out=None, stream=None):
+        """q [N][Hq][D], k and v [N][H][D] of the step's tokens, unrotated:
+        appends k and v and returns the attention output [N][Hq][D]."""
+        qr = self.cache.append(k, v, tok_offsets, positions, k_weight, q, q_weight, self.eps,
+                               self.rope_base, None, stream)
+        return self.attn(qr, tok_offsets, self.cache, parents, self.k_mem, self.v_mem,
+                         self.mem_len, 0.0, out, stream)
 
 
 class HostStream:

@@ -18,6 +18,9 @@ msa_backward
     The backward pass of chunk pooling and routing (gradients of the token
     tensors and of the routing query / bank from the gradients of the pooled
     bank and of the document scores), for training with a routing loss.
+msa_generation
+    The generation step: per-head norms with RoPE and their gradient, the
+    paged append, attention for drafted trees over [memory ; cache ; tree].
 """
 
 from .msa_oracle import (  # noqa: F401
@@ -44,4 +47,13 @@ from .msa_backward import (  # noqa: F401,E402
     encode_pool_backward,
     route_argmax,
     route_scores_backward,
+)
+from .msa_generation import (  # noqa: F401,E402
+    ancestors,
+    head_norm,
+    norm_rope,
+    norm_rope_backward,
+    paged_append,
+    paged_rows,
+    tree_attn,
 )
