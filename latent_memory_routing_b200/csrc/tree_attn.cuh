@@ -132,4 +132,9 @@ __device__ __forceinline__ bool tree_bit(const uint4& m, int j) {
   return (w >> (j & 31)) & 1;
 }
 
+// bf16 on the tensor cores (tree_attn_tc.cu): any shape the entry point
+// takes.  The workspace depends on n_max, G = Hq / H and D.
+size_t tree_tc_workspace_size(int n_max, int G, int D);
+int tree_tc_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);
+
 }  // namespace msa

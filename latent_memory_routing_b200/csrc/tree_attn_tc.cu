@@ -1,0 +1,976 @@
+// bf16 attention for drafted token trees over [memory ; paged cache ; drafted
+// tokens] on the tcgen05 tensor cores (method and semantics: tree_attn.cu).
+//
+// Mathematics.  The query rows of a KV head are (token, head of the group)
+// pairs, R = n G of them; every row sees the same memory and cached keys, and
+// of the drafted keys the bits of its ancestor set.  One pass over the keys
+// with a running maximum and sum:
+//   S = Q K^T (fp32), p = 2^(scale log2(e) s - m), O += bf16(p) V, l += p.
+//
+// What bounds it.  K and V are read once, 4 D bytes a key and KV head, for
+// 4 R D operations: HBM up to about R = 256 rows, beyond that the tensor
+// cores and the exponentials.  So the same tile shape serves all R: rows
+// padded to the MMA's M = 128 cost tensor time that the stream hides.
+//
+// Design.
+//   * Even work: the 128-key tiles of all (sequence, KV head, row block)
+//     items in one line, cut into one contiguous range a CTA (one CTA an SM).
+//     An item inside one range is written directly; an item cut by a range
+//     border is written as fp32 partials (at most two a CTA) that a second
+//     launch merges in a fixed order.  The lengths stay on the device: every
+//     CTA finds its range by a scan over the sequences.
+//   * Two streams, each with its S tile (128 TMEM columns, overwritten by P
+//     in bf16), its O accumulator (D columns) and its softmax warpgroup (a
+//     thread a row).  Up to 128 rows (kQT = 1) the streams take the key tiles
+//     in turn and join their (m, l, O) at an item's end, so a stream has the
+//     time of two tiles; above (kQT = 2) each holds 128 of an item's 256 rows
+//     and both read the same tile.
+//   * Warp 0 loads K tiles, warp 3 V tiles (rings of their own: a K slot is
+//     free after S, a V slot after P V), one lane a page (or 32 memory rows):
+//     only pages that hold rows are read.  Warp 2 walks the range, publishes
+//     the items and copies their query rows into swizzled shared memory.
+//     Warp 1 issues both MMAs, whichever is ready first.
+//   * In a tile that reaches past the sequence's rows or into its drafted
+//     rows, scores outside a row's 128-bit visibility mask become -inf, V
+//     rows past the end are zeroed and non-finite drafted values taken out of
+//     V (0 times them would reach every row); the rows that do see such a
+//     token get it added at the end.
+//   * Every wait is bounded; after a timeout all roles leave their loops.
+#include <algorithm>
+#include <cmath>
+
+#include "attn_tc.cuh"
+#include "tc_ptx.cuh"
+#include "tree_attn.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kMemRows = 32;    // memory rows of one load
+constexpr int kTcThreads = 384; // 4 single warps, 2 softmax warpgroups
+constexpr int kMaxSt = 6;       // K or V ring slots at most
+constexpr int kSched = 3;       // published items
+constexpr int kReaders = 11;    // K warp, V warp, MMA, 8 softmax warps
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kSmemMax = 227 * 1024;
+
+template <int D> struct TC {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kKeys * 128;  // a K or V tile
+  static constexpr uint32_t IDESC_S = tc::idesc_bf16_f32(128, kKeys);
+  static constexpr uint32_t IDESC_O = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V MN-major
+  // registers: 128 x LOW + 256 x HIGH = 384 x 168, the launch's allocation
+  static constexpr int REG_LOW = 88, REG_HIGH = 208;
+  static_assert(128 * REG_LOW + 256 * REG_HIGH == 384 * 168, "register split");
+};
+
+// A CTA's share of one item: key tiles [j_lo, j_lo + cnt) of a row block.
+struct ItemE {
+  int64_t t0;             // the sequence's first token
+  int n, M, L, cache;     // as TreeSeq
+  int b, g, row0, rows;   // row block: rows [row0, row0 + rows) of the n * G
+  int j_lo, cnt;          // cnt < 0: no more items
+  int part;               // partial slot, -1: the whole item, written directly
+};
+
+// What the merging launch needs of the item whose first border lies at a
+// CTA's range start: parts (cta - 1, slot 1), (cta .. last, slot 0).
+struct CutE {
+  int64_t t0;
+  int g, row0, rows, last;  // last < 0: nothing to merge here
+};
+
+struct Aux {
+  uint64_t kfull[kMaxSt], kfree[kMaxSt], vfull[kMaxSt], vfree[kMaxSt];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_empty[2], ml_full;
+  uint64_t sched_full[kSched], sched_empty[kSched];
+  ItemE item[kSched];
+  int bad[kSched];             // item ordinal + 1 where V held non-finite drafted values
+  float2 ml[128];              // (m, l) of the stream that does not finish the item
+  signed char par[kSched][128];  // the published items' parents: -1 root, -2 pruned
+  int64_t start;               // first tile of the range within its sequence
+  int start_b;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+// two Q buffers of 128 rows and five ring slots of 32 KB leave it this much
+static_assert(sizeof(Aux) <= 2048, "shared memory");
+
+__device__ __forceinline__ float ex2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ unsigned long long f2(float lo, float hi) {
+  return (unsigned long long)__float_as_uint(lo) | ((unsigned long long)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// A bf16 pair with its non-finite halves (exponent all ones) replaced by 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+using u128 = unsigned __int128;
+__device__ __forceinline__ u128 low_bits(int n) {  // bits 0 .. n-1
+  return n <= 0 ? (u128)0 : n >= 128 ? ~(u128)0 : (((u128)1 << n) - 1);
+}
+
+// Tiles of one row block of a sequence, and its row blocks.
+__device__ __forceinline__ int seq_tiles(const TreeSeq& s) {
+  return s.n == 0 ? 0 : (s.M + kKeys - 1) / kKeys + (s.cache + kKeys - 1) / kKeys;
+}
+
+template <int D, int kQT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant__ CUtensorMap tm_vm,
+               const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
+               const __grid_constant__ TreeArgs a, int part_rows, int q_rows, int n_k,
+               int n_v, float* __restrict__ part_o, float2* __restrict__ part_ml,
+               CutE* __restrict__ cuts) {
+  using C = TC<D>;
+  constexpr int KB = C::KB;
+  constexpr int kBlkRows = 128 * kQT;
+  pdl_wait();
+  extern __shared__ __align__(1024) unsigned char dsm[];
+  unsigned char* base = tc::smem_align<1024>(dsm);
+  // Q: two buffers of q_rows rows by item (kQT = 1), or two tiles of 128
+  const int q_tile = KB * q_rows * 128;
+  unsigned char* sQ = base;
+  unsigned char* sK = sQ + 2 * q_tile;
+  unsigned char* sV = sK + n_k * C::TILE;
+  Aux& aux = *reinterpret_cast<Aux*>(sV + n_v * C::TILE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.G;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSt; ++i) {
+      tc::mbar_init(&aux.kfull[i], 1);
+      tc::mbar_init(&aux.kfree[i], 1);
+      tc::mbar_init(&aux.vfull[i], 1);
+      tc::mbar_init(&aux.vfree[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&aux.q_full[i], 1);
+      tc::mbar_init(&aux.q_free[i], 1);
+      tc::mbar_init(&aux.s_full[i], 1);
+      tc::mbar_init(&aux.p_full[i], 4);
+      tc::mbar_init(&aux.o_full[i], 1);
+      tc::mbar_init(&aux.o_empty[i], 4);
+    }
+    tc::mbar_init(&aux.ml_full, 4);
+    for (int i = 0; i < kSched; ++i) {
+      tc::mbar_init(&aux.sched_full[i], 1);
+      tc::mbar_init(&aux.sched_empty[i], kReaders);
+      aux.bad[i] = 0;
+    }
+    aux.abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&aux.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+
+  // This CTA's range: thread t sums the tiles of its run of sequences, a scan
+  // over the threads places them, and the thread that holds the range's first
+  // tile finds its sequence.
+  auto tiles_of = [&](const TreeSeq& s) -> int64_t {
+    return (int64_t)seq_tiles(s) * ((s.n * G + kBlkRows - 1) / kBlkRows) * a.H;
+  };
+  int64_t* wsum = reinterpret_cast<int64_t*>(sK);  // [12], before any tile lands there
+  const int per = (a.B + kTcThreads - 1) / kTcThreads;
+  const int b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const TreeSeq s = tree_seq(a, b);
+    if (s.error && blockIdx.x == 0) record_error(a.status, s.error);
+    mine += tiles_of(s);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kTcThreads / 32; ++i) {
+    if (i < warp) before += wsum[i];
+    total += wsum[i];
+  }
+  const int64_t ge = min((int64_t)gridDim.x, total);  // ranges that hold tiles
+  auto range_lo = [&](int64_t c) { return c * total / ge; };
+  const int64_t lo = blockIdx.x < ge ? range_lo(blockIdx.x) : 0;
+  const int64_t hi = blockIdx.x < ge ? range_lo(blockIdx.x + 1) : 0;
+  int64_t at = before + incl - mine;
+  if (lo < hi && lo >= at && lo < at + mine) {
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int64_t t = tiles_of(tree_seq(a, b));
+      if (lo < at + t) {
+        aux.start_b = b;
+        aux.start = lo - at;
+        break;
+      }
+      at += t;
+    }
+  }
+  tc::fence_proxy_async_smem();  // wsum's reads and writes before the tile loads
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = aux.tmem_base;
+  // TMEM columns: S of stream s at 128 s, O at 256 + D s
+  volatile int* abort_flag = &aux.abort_flag;
+  auto fail = [&]() {
+    record_error(a.status, MSA_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (tc::mbar_wait(bar, parity)) return true;
+    fail();
+    return false;
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::REG_LOW));
+    if (warp == 2) {
+      // --------------------------------------------- the range and the queries
+      int64_t left = hi - lo;
+      int b = 0, item = 0, j = 0;
+      TreeSeq s{};
+      int nt = 0, nblk = 0;
+      auto load_seq = [&]() {
+        s = tree_seq(a, b);
+        nt = seq_tiles(s);
+        nblk = (s.n * G + kBlkRows - 1) / kBlkRows;
+      };
+      CutE cut{0, 0, 0, 0, -1};
+      if (left > 0) {
+        b = aux.start_b;
+        load_seq();
+        item = (int)(aux.start / nt);
+        j = (int)(aux.start % nt);
+        if (j > 0 && range_lo(blockIdx.x - 1) <= lo - j) {
+          // the first border inside this item: its last part holds tile `end`
+          const int64_t end = lo - j + nt - 1;
+          int64_t c = min(ge - 1, end * ge / total);
+          while (c + 1 < ge && range_lo(c + 1) <= end) ++c;
+          while (range_lo(c) > end) --c;
+          cut.last = (int)c;
+          cut.t0 = s.t0;
+          cut.g = item / nblk;
+          cut.row0 = item % nblk * kBlkRows;
+          cut.rows = min(kBlkRows, s.n * G - cut.row0);
+        }
+      }
+      if (lane == 0) cuts[blockIdx.x] = cut;
+      for (uint32_t k = 0;; ++k) {
+        const int slot = k % kSched;
+        if (!wait(&aux.sched_empty[slot], ((k / kSched) & 1) ^ 1)) break;
+        ItemE e{};
+        e.cnt = -1;
+        if (left > 0) {
+          while (item == a.H * nblk || nt == 0) {  // the next sequence with tiles
+            ++b;
+            load_seq();
+            item = 0;
+          }
+          e.t0 = s.t0;
+          e.n = s.n;
+          e.M = s.M;
+          e.L = s.L;
+          e.cache = s.cache;
+          e.b = b;
+          e.g = item / nblk;
+          e.row0 = item % nblk * kBlkRows;
+          e.rows = min(kBlkRows, s.n * G - e.row0);
+          e.j_lo = j;
+          e.cnt = (int)min((int64_t)(nt - j), left);
+          e.part = j > 0 ? 0 : e.cnt < nt ? 1 : -1;
+          left -= e.cnt;
+          ++item;
+          j = 0;
+        }
+        if (a.parents && e.cnt > 0) {
+          for (int i = lane; i < e.n; i += 32) {
+            int p = a.parents[e.t0 + i];
+            if (p >= i) {  // a parent comes before its child
+              record_error(a.status, MSA_ERR_INVALID_ARG);
+              p = -2;
+            }
+            aux.par[slot][i] = (signed char)max(p, -2);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          aux.item[slot] = e;
+          tc::mbar_arrive(&aux.sched_full[slot]);
+        }
+        if (e.cnt < 0) break;
+        // its query rows, into buffer k & 1 (kQT = 1) or the two tiles
+        const int qb = kQT == 1 ? k & 1 : 0;
+        const uint32_t use = kQT == 1 ? k >> 1 : k;
+        if (use > 0 && !wait(&aux.q_free[qb], (use - 1) & 1)) break;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        for (int c = lane; c < e.rows * (D / 8); c += 32) {
+          const int r = c / (D / 8), ch = c % (D / 8);
+          const int row = e.row0 + r;
+          const __nv_bfloat16* src =
+              q + ((e.t0 + row / G) * a.Hq + e.g * G + row % G) * D + ch * 8;
+          const int tile = kQT == 1 ? qb : r >> 7, rr = kQT == 1 ? r : r & 127;
+          unsigned char* dst = sQ + tile * q_tile + (ch >> 3) * (q_rows * 128) + rr * 128 +
+                               (((ch & 7) ^ (rr & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)),
+                       "l"(src)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&aux.q_full[qb]);
+      }
+    } else if (warp == 0 || warp == 3) {
+      // ----------------------------------------------------------- K, V loads
+      const bool isv = warp == 3;
+      unsigned char* ring = isv ? sV : sK;
+      uint64_t* full = isv ? aux.vfull : aux.kfull;
+      uint64_t* fre = isv ? aux.vfree : aux.kfree;
+      const int n_st = isv ? n_v : n_k;
+      const CUtensorMap* mm = isv ? &tm_vm : &tm_km;
+      const CUtensorMap* mp = isv ? &tm_vp : &tm_kp;
+      const int page = a.page_size;
+      int st = 0;
+      uint32_t ph = 0, loads = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const int slot = k % kSched;
+        if (!wait(&aux.sched_full[slot], (k / kSched) & 1)) break;
+        const ItemE e = aux.item[slot];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&aux.sched_empty[slot]);
+        if (e.cnt < 0) break;
+        const int n_mt = (e.M + kKeys - 1) / kKeys;
+        const int32_t* table = a.block_table + (int64_t)e.b * a.max_pages;
+        // the first tensor-map row of this lane's piece of tile j, -1: none
+        auto piece = [&](int j) -> int {
+          if (j < n_mt) {
+            const int r0 = j * kKeys + lane * kMemRows;
+            return lane < kKeys / kMemRows && r0 < e.M ? e.b * a.m_cap + r0 : -1;
+          }
+          const int r0 = (j - n_mt) * kKeys + lane * page;
+          if (lane * page >= kKeys || r0 >= e.cache) return -1;
+          const int pg = table[r0 / page];
+          if (pg < 0 || pg >= a.n_pages) {
+            record_error(a.status, MSA_ERR_INVALID_ARG);
+            return -1;
+          }
+          return (pg * a.H + e.g) * page;
+        };
+        int next = piece(e.j_lo);
+        for (int i = 0; i < e.cnt; ++i) {
+          const int j = e.j_lo + i, row = next;
+          if (i + 1 < e.cnt) next = piece(j + 1);  // in flight while the slot drains
+          const bool mem = j < n_mt;
+          const int rows = mem ? kMemRows : page;
+          ok = wait(&fre[st], ph ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+          if (lane == 0)
+            tc::mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(live) * rows * 128 * KB);
+          __syncwarp();
+          if (row >= 0) {
+            unsigned char* d = ring + st * C::TILE + lane * rows * 128;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              tc::tma_load_3d(d + kb * kKeys * 128, mem ? mm : mp, &full[st], kb * 64,
+                              mem ? e.g : 0, row);
+          }
+          ++loads;
+          if (++st == n_st) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // every load issued lands before the CTA exits
+      for (uint32_t v = loads > (uint32_t)n_st ? loads - n_st : 0; v < loads; ++v)
+        tc::mbar_wait(&full[v % n_st], (v / n_st) & 1);
+    } else if (lane == 0) {
+      // ----------------------------------------------------------------- MMA
+      // Virtual tile v belongs to stream v & 1: key tile v (kQT = 1) or
+      // v >> 1 (kQT = 2) of the range.  S(v) may follow once P V(v - 2),
+      // which reads the same TMEM columns, has been issued (one thread's
+      // MMAs run in issue order), so S(v)'s commit also says that P V(v - 2)
+      // is done.  P V and S are issued as they become ready.
+      struct Walk {
+        uint32_t k;     // items taken
+        int i, cnt;     // key tile within the item's share
+      };
+      Walk ws{0, 0, 0}, wp{0, 0, 0};
+      uint32_t vs = 0, vp = 0;   // S and P V issued
+      uint32_t ne[2] = {0, 0};   // items whose O a stream has begun
+      int kst = 0, vst = 0;      // ring slots of the next S and P V
+      uint32_t kph = 0, vph = 0;
+      bool have = false, done = false;
+      uint64_t t_last = tc::globaltimer_ns();
+      uint32_t polls = 0;
+      while (!(done && vp == vs)) {
+        bool moved = false;
+        if (vp < vs) {
+          const int s = vp & 1;
+          if (tc::mbar_test(&aux.p_full[s], (vp >> 1) & 1)) {
+            if (wp.i == wp.cnt) {  // published: S has read it
+              const int slot = wp.k % kSched;
+              wp.cnt = aux.item[slot].cnt;
+              wp.i = 0;
+              ++wp.k;
+              tc::mbar_arrive(&aux.sched_empty[slot]);
+            }
+            const bool first = kQT == 1 ? wp.i < 2 : wp.i == 0;
+            const bool last = kQT == 1 ? wp.i + 2 >= wp.cnt : wp.i + 1 == wp.cnt;
+            if ((!first || ne[s] == 0 || tc::mbar_test(&aux.o_empty[s], (ne[s] - 1) & 1)) &&
+                tc::mbar_test(&aux.vfull[vst], vph)) {
+              if (first) ++ne[s];
+              tc::tc_fence_after();
+              const uint64_t vd =
+                  tc::sdesc_mnmajor_sw128(tc::smem_u32(sV + vst * C::TILE), kKeys * 128);
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc::mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8,
+                                tc::desc_add(vd, kk * 16 * 128), C::IDESC_O,
+                                (!first || kk > 0) ? 1u : 0u);
+              if (last) tc::mma_commit(&aux.o_full[s]);
+              if (kQT == 1 || s == 1) {
+                tc::mma_commit(&aux.vfree[vst]);
+                if (++vst == n_v) {
+                  vst = 0;
+                  vph ^= 1;
+                }
+                ++wp.i;
+              }
+              ++vp;
+              moved = true;
+            }
+          }
+        }
+        if (!done && vs < vp + 2) {
+          if (!have && tc::mbar_test(&aux.sched_full[ws.k % kSched], (ws.k / kSched) & 1)) {
+            ws.cnt = aux.item[ws.k % kSched].cnt;
+            ws.i = 0;
+            have = ws.cnt > 0;
+            done = !have;
+            ++ws.k;
+            moved = true;
+          }
+          if (have) {
+            const uint32_t ord = ws.k - 1;
+            const int qb = kQT == 1 ? ord & 1 : 0;
+            const uint32_t use = kQT == 1 ? ord >> 1 : ord;
+            if (tc::mbar_test(&aux.q_full[qb], use & 1) && tc::mbar_test(&aux.kfull[kst], kph)) {
+              const int s = vs & 1;
+              tc::tc_fence_after();
+              const uint64_t qd = tc::sdesc_kmajor_sw128(
+                  tc::smem_u32(sQ + (kQT == 1 ? qb : s) * q_tile));
+              const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(sK + kst * C::TILE));
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_bf16_ss(tmem + s * 128,
+                                tc::desc_add(qd, (kk >> 2) * (q_rows * 128) + (kk & 3) * 32),
+                                tc::desc_add(kd, (kk >> 2) * (kKeys * 128) + (kk & 3) * 32),
+                                C::IDESC_S, kk > 0 ? 1u : 0u);
+              tc::mma_commit(&aux.s_full[s]);
+              if (kQT == 1 || s == 1) {
+                tc::mma_commit(&aux.kfree[kst]);
+                if (++kst == n_k) {
+                  kst = 0;
+                  kph ^= 1;
+                }
+                if (++ws.i == ws.cnt) {
+                  tc::mma_commit(&aux.q_free[qb]);
+                  have = false;
+                }
+              }
+              ++vs;
+              moved = true;
+            }
+          }
+        }
+        if (moved) {
+          polls = 0;
+        } else {
+          if (polls == 0) t_last = tc::globaltimer_ns();
+          if ((++polls & 255u) == 0) {
+            if (*abort_flag) break;
+            if (tc::globaltimer_ns() - t_last > 2000000000ull) {
+              fail();
+              break;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::REG_HIGH));
+    const int grp = (warp - 4) >> 2;   // stream
+    const int quad = warp & 3;         // TMEM lane quarter
+    const int r = quad * 32 + lane;    // row of the stream's tile; V row to clean
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    const uint32_t tSP = tmem + grp * 128 + lane_addr;
+    const float qscale = a.qscale;
+    uint32_t w = 0;           // tiles of this stream so far
+    uint32_t u = 0;           // key tiles of the CTA so far
+    uint32_t ne[2] = {0, 0};  // items whose O a stream has held
+    uint32_t n_pub = 0;
+    for (uint32_t k = 0;; ++k) {
+      const int slot = k % kSched;
+      if (!wait(&aux.sched_full[slot], (k / kSched) & 1)) break;
+      const ItemE e = aux.item[slot];
+      if (e.cnt < 0) break;
+      const int i0 = kQT == 1 ? (u ^ grp) & 1 : 0;
+      const int step = kQT == 1 ? 2 : 1;
+      const bool both = kQT == 1 && e.cnt >= 2;     // both streams hold a part of O
+      const int owner = kQT == 1 ? (u + e.cnt - 1) & 1 : grp;
+      const int rb = (kQT == 2 ? grp * 128 : 0) + r;  // row within the block
+      const bool row_ok = rb < e.rows;
+      const bool warp_on = (kQT == 2 ? grp * 128 : 0) + quad * 32 < e.rows;
+      const int row = e.row0 + rb;
+      const int tok = row / G;
+      u128 anc = 0;
+      if (i0 < e.cnt) {
+        // what the row's token sees of its tree
+        if (!a.parents) {
+          anc = low_bits(tok + 1);
+        } else if (row_ok) {
+          const signed char* par = aux.par[slot];
+          int x = tok;
+          do {
+            anc |= (u128)1 << x;
+            x = par[x];
+          } while (x >= 0);
+          if (x != -1) anc = 0;  // pruned: sees nothing
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&aux.sched_empty[slot]);
+      if (i0 < e.cnt) {
+        const bool dead = anc == 0;
+        const int n_mt = (e.M + kKeys - 1) / kKeys;
+        float m_run = -INFINITY, l_run = 0.f;
+        for (int i = i0, t = 0; i < e.cnt; i += step, ++t, ++w) {
+          const int j = e.j_lo + i;
+          const bool mem = j < n_mt;
+          const int key0 = (mem ? j : j - n_mt) * kKeys;
+          const int n_rows = mem ? e.M - key0 : e.cache - key0;  // rows of the tile that exist
+          const bool full = key0 + kKeys <= (mem ? e.M : e.L);   // every row sees every key
+          if (!wait(&aux.s_full[grp], w & 1)) break;
+          tc::tc_fence_after();
+          if (!full && (kQT == 1 || grp == 0) && (n_rows < kKeys || e.n > 1)) {
+            // V(u + i) has landed at most once since P V of the slot's last
+            // tile, so the parity names this tile; P V waits for this
+            // group's p_full below
+            const uint32_t vi = u + i;
+            if (!wait(&aux.vfull[vi % n_v], (vi / n_v) & 1)) break;
+            unsigned char* vr = sV + (vi % n_v) * C::TILE + r * 128;
+            if (r >= n_rows) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4)) =
+                    make_uint4(0, 0, 0, 0);
+            } else if (!mem && key0 + r >= e.L) {
+              bool bad = false;
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* p =
+                    reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4));
+                const uint4 x = *p;
+                const uint4 y =
+                    make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+                if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+                  *p = y;
+                  bad = true;
+                }
+              }
+              if (bad) *(volatile int*)&aux.bad[k % kSched] = (int)k + 1;
+            }
+            tc::fence_proxy_async_smem();
+          }
+          if (warp_on) {
+            uint32_t sv[kKeys];
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c)
+              tc::tmem_ld32(tSP + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + c * 32));
+            tc::tmem_ld_wait();
+            if (!full) {
+              u128 vis;
+              if (mem) {
+                vis = low_bits(n_rows);
+              } else {
+                const int off = e.L - key0;  // column of the first drafted key
+                vis = low_bits(off) | (off >= 0 ? (off < 128 ? anc << off : (u128)0)
+                                                : (off > -128 ? anc >> -off : (u128)0));
+                vis &= low_bits(n_rows);
+              }
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                const uint32_t bits = (uint32_t)(vis >> (32 * q4));
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((bits >> c) & 1)) sv[32 * q4 + c] = 0xff800000u;
+              }
+            }
+            // row maximum: 8 chains of 3-input max
+            float mx[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(sv[c]);
+#pragma unroll
+            for (int c = 8; c + 16 <= kKeys; c += 16)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                mx[x] = fmax3(mx[x], __uint_as_float(sv[c + x]), __uint_as_float(sv[c + 8 + x]));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(sv[kKeys - 8 + x]));
+            const float mt = qscale * fmax3(fmax3(mx[0], mx[1], mx[2]),
+                                            fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            // the reference maximum moves only when a tile exceeds it by 2^8
+            const bool grow = row_ok && mt > m_run + kRescaleLog2;
+            float alpha = 1.f;
+            if (grow) {
+              alpha = m_run == -INFINITY ? 0.f : ex2a(m_run - mt);
+              m_run = mt;
+            }
+            if (t > 0 && __any_sync(0xffffffffu, grow && alpha != 0.f)) {
+              const uint32_t tO = tmem + 256 + grp * D + lane_addr;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc::tmem_ld32(tO + c * 32, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                tmem_st32(tO + c * 32, o);
+              }
+            }
+            l_run *= alpha;
+            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+            const unsigned long long sc2 = f2(qscale, qscale), nm2 = f2(neg_m, neg_m);
+            unsigned long long ls2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < kKeys / 64; ++c) {
+              uint32_t pw[32];
+#pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                const int k0 = c * 64 + 2 * x;
+                unsigned long long x2 =
+                    (unsigned long long)sv[k0] | ((unsigned long long)sv[k0 + 1] << 32);
+                asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x2) : "l"(sc2), "l"(nm2));
+                const float p0 = ex2a(__uint_as_float((uint32_t)x2));
+                const float p1 = ex2a(__uint_as_float((uint32_t)(x2 >> 32)));
+                const unsigned long long p2 = f2(p0, p1);
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(ls2[x & 1]) : "l"(p2));
+                pw[x] = pack2(p0, p1);
+              }
+              tmem_st32(tSP + c * 32, pw);
+            }
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(ls2[0]) : "l"(ls2[1]));
+            l_run += __uint_as_float((uint32_t)ls2[0]) + __uint_as_float((uint32_t)(ls2[0] >> 32));
+            tmem_st_wait();
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&aux.p_full[grp]);
+        }
+        if (dead) {
+          m_run = -INFINITY;
+          l_run = 0.f;
+        }
+        if (owner != grp) {
+          // hand (m, l) to the other group, which reads this stream's O too
+          if (ne[grp] > 0 && !wait(&aux.o_empty[grp], (ne[grp] - 1) & 1)) break;
+          aux.ml[r] = make_float2(m_run, l_run);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&aux.ml_full);
+        } else {
+          if (!wait(&aux.o_full[grp], ne[grp] & 1)) break;
+          float c0 = 1.f, c1 = 0.f;
+          bool use0 = l_run != 0.f, use1 = false;
+          if (both) {
+            if (!wait(&aux.o_full[grp ^ 1], ne[grp ^ 1] & 1)) break;
+            if (!wait(&aux.ml_full, n_pub & 1)) break;
+            const float2 x = aux.ml[r];
+            const float m = fmaxf(m_run, x.x);
+            c0 = m == -INFINITY ? 1.f : ex2a(m_run - m);
+            c1 = m == -INFINITY ? 1.f : ex2a(x.x - m);
+            use1 = x.y != 0.f;
+            l_run = (use0 ? c0 * l_run : 0.f) + (use1 ? c1 * x.y : 0.f);
+            m_run = m;
+          }
+          tc::tc_fence_after();
+          const bool bad = *(volatile int*)&aux.bad[k % kSched] == (int)k + 1;
+          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+          const int64_t orow = (e.t0 + tok) * a.Hq + e.g * G + row % G;
+          const int64_t prow = ((int64_t)blockIdx.x * 2 + e.part) * part_rows + rb;
+          if (warp_on) {
+            const uint32_t tO = tmem + 256 + grp * D + lane_addr;
+            const uint32_t tO2 = tmem + 256 + (grp ^ 1) * D + lane_addr;
+            // unrolled only as far as registers allow
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x0[32], x1[32];
+              float o[32];
+              tc::tmem_ld32(tO + c * 32, x0);
+              if (both) tc::tmem_ld32(tO2 + c * 32, x1);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                o[x] = use0 ? c0 * __uint_as_float(x0[x]) : 0.f;
+                if (both) o[x] += use1 ? c1 * __uint_as_float(x1[x]) : 0.f;
+              }
+              if (row_ok) {
+                if (bad) {
+                  // drafted values taken out of V, for the rows that see them
+                  for (int d = 0; d < e.n; ++d) {
+                    const int kr = e.L + d, j = n_mt + kr / kKeys;
+                    if (!((anc >> d) & 1) || j < e.j_lo || j >= e.j_lo + e.cnt || kr >= e.cache)
+                      continue;
+                    const int pg = a.block_table[(int64_t)e.b * a.max_pages + kr / a.page_size];
+                    if (pg < 0 || pg >= a.n_pages) continue;
+                    const __nv_bfloat16* v =
+                        static_cast<const __nv_bfloat16*>(a.v_pages) +
+                        (((int64_t)pg * a.H + e.g) * a.page_size + kr % a.page_size) * D + c * 32;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                      const float f = __bfloat162float(v[x]);
+                      if (!isfinite(f)) o[x] += f;
+                    }
+                  }
+                }
+                if (e.part < 0) {
+                  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32;
+#pragma unroll
+                  for (int x = 0; x < 32; x += 8)
+                    st16(op + x, make_uint4(pack2(o[x] * inv, o[x + 1] * inv),
+                                            pack2(o[x + 2] * inv, o[x + 3] * inv),
+                                            pack2(o[x + 4] * inv, o[x + 5] * inv),
+                                            pack2(o[x + 6] * inv, o[x + 7] * inv)));
+                } else {
+                  float* po = part_o + prow * D + c * 32;
+#pragma unroll
+                  for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<float4*>(po + x) =
+                        make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                }
+              }
+              __syncwarp();  // the next load is the whole warp's
+            }
+            if (row_ok && e.part >= 0) part_ml[prow] = make_float2(m_run, l_run);
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&aux.o_empty[grp]);
+            if (both) tc::mbar_arrive(&aux.o_empty[grp ^ 1]);
+          }
+        }
+      }
+      if (kQT == 1) {
+        ++ne[u & 1];
+        if (both) {
+          ++ne[(u & 1) ^ 1];
+          ++n_pub;
+        }
+      } else {
+        ++ne[grp];
+      }
+      u += e.cnt;
+    }
+  }
+
+  pdl_trigger();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merges the parts of the items cut by range borders.  blockIdx.x: the border
+// before that CTA's range; blockIdx.y: kRowsBlk rows of the item.  Four warps:
+// one row each (many rows), or one row between them, each a quarter of the
+// parts (few rows: the parts' loads then overlap).
+template <int D, bool kFewRows>
+__global__ void __launch_bounds__(128)
+tree_merge_kernel(const __grid_constant__ TreeArgs a, int part_rows,
+                  const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                  const CutE* __restrict__ cuts) {
+  constexpr int VEC = D / 32;
+  __shared__ float so[4][D];
+  __shared__ float2 sml[4];
+  pdl_trigger();
+  pdl_wait();
+  const CutE cut = cuts[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = kFewRows ? blockIdx.y : blockIdx.y * 4 + warp;
+  if (cut.last < 0 || rr >= cut.rows) return;
+  const int n_parts = cut.last - (int)blockIdx.x + 2;
+  float m = -INFINITY, l = 0.f, o[VEC];
+#pragma unroll
+  for (int x = 0; x < VEC; ++x) o[x] = 0.f;
+  // part 0 is slot 1 of the CTA before the border, part i slot 0 of the
+  // i - 1st after it
+  auto prow = [&](int i) {
+    const int64_t cta = (int64_t)blockIdx.x - 1 + i;
+    return (cta * 2 + (i == 0 ? 1 : 0)) * part_rows + rr;
+  };
+  auto join = [&](float2 ml, const float* v) {
+    if (ml.y == 0.f) return;
+    const float mn = fmaxf(m, ml.x);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float c0 = exp2f(m - ref), c1 = ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref);
+    l = (l == 0.f ? 0.f : l * c0) + ml.y * c1;
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) o[x] = o[x] * c0 + v[x] * c1;
+    m = mn;
+  };
+  const int step = kFewRows ? 4 : 1;
+  for (int i = kFewRows ? warp : 0; i < n_parts; i += 4 * step) {
+    float2 ml[4];
+    float v[4][VEC];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int p = i + x * step;
+      ml[x] = make_float2(-INFINITY, 0.f);
+      if (p < n_parts) {
+        const int64_t pr = prow(p);
+        ml[x] = part_ml[pr];
+        const float* src = part_o + pr * D + lane * VEC;
+#pragma unroll
+        for (int y = 0; y < VEC; ++y) v[x][y] = src[y];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) join(ml[x], v[x]);
+  }
+  if (kFewRows) {
+    if (lane == 0) sml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) so[warp][lane * VEC + x] = o[x];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) join(sml[i], &so[i][lane * VEC]);
+  }
+  const int row = cut.row0 + rr;
+  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
+                      ((cut.t0 + row / a.G) * a.Hq + cut.g * a.G + row % a.G) * D + lane * VEC;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int x = 0; x < VEC; x += 2)
+    *reinterpret_cast<uint32_t*>(op + x) =
+        l == 0.f ? 0u : pack2(o[x] * inv, o[x + 1] * inv);
+}
+
+struct TcPlan {
+  int qt;          // Q tiles of an item
+  int part_rows;   // rows of a partial
+  int q_rows, n_k, n_v;
+  size_t smem, po_bytes, ml_bytes, cut_bytes, total;
+};
+
+// kQT = 2 once an item's rows exceed one MMA tile: both tiles then share one
+// pass over K and V.  The Q buffers hold no more rows than a sequence can
+// have (the MMA reads on into the ring: rows of S that nobody reads), what
+// they leave goes to the rings.
+TcPlan tc_plan(int n_max, int G, int D) {
+  TcPlan p{};
+  const int rows = n_max * G;
+  p.qt = rows > 128 ? 2 : 1;
+  p.part_rows = std::min(rows, 128 * p.qt);
+  p.q_rows = p.qt == 2 ? 128 : (rows + 7) / 8 * 8;
+  const int tile = D / 64 * kKeys * 128;
+  const int q_bytes = 2 * (D / 64) * p.q_rows * 128;
+  const int slots = (kSmemMax - 1024 - (int)sizeof(Aux) - q_bytes) / tile;
+  p.n_v = std::min(kMaxSt, (slots + 1) / 2);
+  p.n_k = std::min(kMaxSt, slots - p.n_v);
+  p.smem = 1024 + q_bytes + (size_t)(p.n_k + p.n_v) * tile + sizeof(Aux);
+  const size_t parts = 2 * (size_t)num_sms() * p.part_rows;
+  p.po_bytes = round_up(parts * D * sizeof(float), 256);
+  p.ml_bytes = round_up(parts * sizeof(float2), 256);
+  p.cut_bytes = round_up((size_t)num_sms() * sizeof(CutE), 256);
+  p.total = p.po_bytes + p.ml_bytes + p.cut_bytes;
+  return p;
+}
+
+template <int D, int kQT>
+int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  float* part_o = reinterpret_cast<float*>(w);
+  float2* part_ml = reinterpret_cast<float2*>(w + p.po_bytes);
+  CutE* cuts = reinterpret_cast<CutE*>(w + p.po_bytes + p.ml_bytes);
+  CUtensorMap km, vm, kp, vp;
+  const int64_t page_rows = (int64_t)a.n_pages * a.H * a.page_size;
+  bool ok = tma_map_sw128_bf16(&kp, a.k_pages, D, 1, page_rows, 1, a.page_size) &&
+            tma_map_sw128_bf16(&vp, a.v_pages, D, 1, page_rows, 1, a.page_size);
+  if (a.m_cap > 0)
+    ok = ok && tma_map_sw128_bf16(&km, a.k_mem, D, a.H, (int64_t)a.B * a.m_cap, 1, kMemRows) &&
+         tma_map_sw128_bf16(&vm, a.v_mem, D, a.H, (int64_t)a.B * a.m_cap, 1, kMemRows);
+  else
+    km = kp, vm = vp;  // never loaded from
+  if (!ok) return note_cuda(cudaErrorInvalidValue);
+  auto kern = tree_tc_kernel<D, kQT>;
+  if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)p.smem)) return rc;
+  const unsigned grid = (unsigned)num_sms();
+  if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, km, vm, kp, vp, a,
+                          p.part_rows, p.q_rows, p.n_k, p.n_v, part_o, part_ml, cuts))
+    return rc;
+  // up to 16 rows: a block a row (a decode step's parts are many and short)
+  if (p.part_rows <= 16)
+    return launch_pdl(tree_merge_kernel<D, true>, dim3(grid, (unsigned)p.part_rows), dim3(128), 0,
+                      s, a, p.part_rows, part_o, part_ml, cuts);
+  return launch_pdl(tree_merge_kernel<D, false>, dim3(grid, (unsigned)((p.part_rows + 3) / 4)),
+                    dim3(128), 0, s, a, p.part_rows, part_o, part_ml, cuts);
+}
+
+}  // namespace
+
+size_t tree_tc_workspace_size(int n_max, int G, int D) { return tc_plan(n_max, G, D).total; }
+
+int tree_tc_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s) {
+  const TcPlan p = tc_plan(a.n_max, a.G, D);
+  if (D == 64) return p.qt == 1 ? launch_tc<64, 1>(a, p, ws, s) : launch_tc<64, 2>(a, p, ws, s);
+  return p.qt == 1 ? launch_tc<128, 1>(a, p, ws, s) : launch_tc<128, 2>(a, p, ws, s);
+}
+
+}  // namespace msa
