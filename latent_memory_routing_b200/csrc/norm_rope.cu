@@ -10,11 +10,16 @@
 //   dw = sum over rows of dz x r.
 //
 // Every row is read once and written once and nothing else is, so HBM
-// bounds all three kernels.  A row's halves are loaded as 16-byte vectors by
-// D / 2 / VEC neighbouring lanes (a thread holds VEC pairs: both partners of
-// each), the mean is a shuffle over those lanes, and a warp works through
-// the heads of one token so that the token's D/2 (cos, sin) are built once
-// (two or fewer a lane, shared through shared memory) for all of them.
+// bounds all three kernels.  A row's halves are 16-byte vectors of D / 2 /
+// VEC neighbouring lanes (a thread holds VEC pairs: both partners of each), so
+// the mean is a shuffle over those lanes and one pass of a warp takes
+// 32 / lanes rows.  What feeds HBM is bytes in flight: a warp walks a
+// contiguous run of tokens and each lane copies its own vectors of the passes
+// to come into its own slots of shared memory (cp.async), kDepth passes
+// ahead, with no barrier between lanes and no registers held (loads straight
+// into registers reached 4.1 TB/s with one pass a warp in flight and 5.1 with
+// five; this 5.9, the gradient 5.8, a plain copy 6.6).  A token's D / 2 (cos, sin) are built once, two or
+// fewer a lane, for all its rows.
 //
 // The angle needs no double arithmetic on the device: the host gives each
 // pair's frequency in turns as a 64-bit binary fraction f, and p * f modulo
@@ -39,49 +44,78 @@ struct TurnTab {
   uint64_t f[kMaxHalf];
 };
 
+// One power a call (64 of them cost the host 15 us): the rest are products,
+// whose relative error grows to i 2^-64, 2^-30 turns at the farthest position.
 TurnTab turn_tab(float base, int D) {
   TurnTab t{};
-  const long double two_pi = 6.283185307179586476925286766559L;
-  for (int i = 0; i < D / 2; ++i) {
-    const long double turns = powl((long double)base, -2.0L * i / D) / two_pi;
+  const long double ratio = powl((long double)base, -2.0L / D);
+  long double turns = 1.0L / 6.283185307179586476925286766559L;
+  for (int i = 0; i < D / 2; ++i, turns *= ratio) {
     const long double frac = turns - floorl(turns);
-    // 2^64 * frac, in two 32-bit steps (frac < 1)
-    const long double hi = floorl(frac * 4294967296.0L);
-    const long double lo = floorl((frac * 4294967296.0L - hi) * 4294967296.0L);
-    t.f[i] = ((uint64_t)hi << 32) | (uint64_t)lo;
+    t.f[i] = (uint64_t)(frac * 18446744073709551616.0L);  // frac < 1 exactly: no overflow
   }
   return t;
 }
 
-// (cos, sin) of position p at frequency f.
-__device__ __forceinline__ float2 turn_cs(int32_t p, uint64_t f) {
-  const uint64_t u = (uint64_t)(int64_t)p * f;
-  const int32_t h = (int32_t)((u + 0x80000000ull) >> 32);  // 2^-32 turns, nearest
-  float s, c;
-  sincospif((float)h * 4.656612873077393e-10f, &s, &c);  // h 2^-31 half turns
-  return make_float2(c, s);
+// 16 bytes into this lane's slot of shared memory.  (Global reads of the L2:
+// an output may alias its input exactly.)
+__device__ __forceinline__ void cp16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// This lane's copies are done but for those of the last N groups.
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Plain (coherent) load that is not kept in L1: an output may alias its
-// input exactly, so the read-only path is not used.
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Two floats in one 64-bit register: the arithmetic below runs on pairs
+// (f32x2 instructions), two elements of a row each.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 mk2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 un2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// N consecutive elements of type E as floats (16-byte aligned).
-template <typename E, int N>
-__device__ __forceinline__ void load_f(const E* p, float* f) {
+// 16 bytes of type E as Vec16<E>::N / 2 pairs, and back.
+template <typename E>
+__device__ __forceinline__ void pairs(const uint4& v, f2* p) {
+  float f[Vec16<E>::N];
+  Vec16<E>::unpack(v, f);
 #pragma unroll
-  for (int i = 0; i < N; i += Vec16<E>::N) Vec16<E>::unpack(ld16(p + i), f + i);
+  for (int i = 0; i < Vec16<E>::N / 2; ++i) p[i] = mk2(f[2 * i], f[2 * i + 1]);
 }
-template <typename E, int N>
-__device__ __forceinline__ void store_f(E* p, const float* f) {
+template <typename E>
+__device__ __forceinline__ uint4 from_pairs(const f2* p) {
+  float f[Vec16<E>::N];
 #pragma unroll
-  for (int i = 0; i < N; i += Vec16<E>::N) st16(p + i, Vec16<E>::pack(f + i));
+  for (int i = 0; i < Vec16<E>::N / 2; ++i) {
+    const float2 x = un2(p[i]);
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
+  }
+  return Vec16<E>::pack(f);
 }
 
 // How a warp's lanes lie over head rows of D elements of type T.
@@ -92,21 +126,119 @@ template <typename T, int D> struct RowMap {
   static constexpr int RPW = 32 / LPR;          // rows a warp
 };
 
-// Sum over the LPR lanes of a row.
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+// (cos, sin) of position p at N frequencies f.  The fraction of a turn, as a
+// 32-bit integer, is cut into the nearest quarter turn and a rest of at most
+// pi / 4, exactly; the rest's Taylor series (sine to x^9, cosine to x^10,
+// errors below 3e-9) run on pairs, and the quarter turns swap and negate.
+template <int N>
+__device__ __forceinline__ void turn_cs(int32_t p, const uint64_t (&f)[N], float (&co)[N],
+                                        float (&si)[N]) {
+  int32_t quarter[2];
+  float x[2] = {0.f, 0.f};
 #pragma unroll
-  for (int o = LPR / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < N; ++i) {
+    const uint64_t u = (uint64_t)(int64_t)p * f[i];
+    const int32_t h = (int32_t)((u + 0x80000000ull) >> 32);  // 2^-32 turns, nearest
+    quarter[i] = (int32_t)((uint32_t)h + 0x20000000u) >> 30;
+    const int32_t rest = (int32_t)((uint32_t)h - ((uint32_t)quarter[i] << 30));
+    x[i] = (float)rest * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  }
+  const f2 y = mk2(x[0], x[1]), z = mul2(y, y);
+  auto k = [](float v) { return mk2(v, v); };
+  f2 a = fma2(z, k(1.f / 362880), k(-1.f / 5040));
+  a = fma2(z, a, k(1.f / 120));
+  a = fma2(z, a, k(-1.f / 6));
+  a = fma2(mul2(y, z), a, y);
+  f2 b = fma2(z, k(-1.f / 3628800), k(1.f / 40320));
+  b = fma2(z, b, k(-1.f / 720));
+  b = fma2(z, b, k(1.f / 24));
+  b = fma2(z, b, k(-.5f));
+  b = fma2(z, b, k(1.f));
+  const float sn[2] = {un2(a).x, un2(a).y}, cn[2] = {un2(b).x, un2(b).y};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool odd = quarter[i] & 1;
+    const uint32_t s_neg = (uint32_t)(quarter[i] & 2) << 30;
+    const uint32_t c_neg = (uint32_t)((quarter[i] + 1) & 2) << 30;
+    si[i] = __uint_as_float(__float_as_uint(odd ? cn[i] : sn[i]) ^ s_neg);
+    co[i] = __uint_as_float(__float_as_uint(odd ? sn[i] : cn[i]) ^ c_neg);
+  }
 }
 
-// The token's (cos, sin) into cs[0 .. D/2), by one warp.
+// The token's angles into cs[0 .. HALF) (cosines) and cs[HALF .. D) (sines),
+// by one warp; f holds the lane's frequencies (read once: the constant bank
+// serves one address at a time).
 template <int HALF>
-__device__ __forceinline__ void token_cs(const TurnTab& tab, int32_t p, float2* cs, int lane) {
+__device__ __forceinline__ void token_cs(const uint64_t (&f)[HALF / 32], int32_t p, float* cs,
+                                         int lane) {
+  float co[HALF / 32], si[HALF / 32];
+  turn_cs(p, f, co, si);
   __syncwarp();  // earlier readers of cs are done
 #pragma unroll
-  for (int i = lane; i < HALF; i += 32) cs[i] = turn_cs(p, tab.f[i]);
+  for (int i = 0; i < HALF / 32; ++i) {
+    cs[i * 32 + lane] = co[i];
+    cs[HALF + i * 32 + lane] = si[i];
+  }
   __syncwarp();
+}
+
+// The passes of a warp, in order: (token, part) work items w, w + step, ..,
+// each a range of the token's row groups.
+struct Passes {
+  int64_t w, w_hi, step, t;
+  int gi, g_hi;
+  __device__ __forceinline__ bool more() const { return w < w_hi; }
+  __device__ __forceinline__ void start(int splits, int groups) {
+    if (splits == 1) {
+      t = w;
+      gi = 0;
+      g_hi = groups;
+    } else {
+      t = w / splits;
+      const int part = (int)(w - t * splits);
+      gi = part * groups / splits;
+      g_hi = (part + 1) * groups / splits;
+    }
+  }
+  // Moves on; true when the next pass begins another work item.
+  __device__ __forceinline__ bool next(int splits, int groups) {
+    if (++gi < g_hi) return false;
+    if ((w += step) < w_hi) start(splits, groups);
+    return true;
+  }
+};
+
+// What warp i of n takes of n_work items: a contiguous share (a long append:
+// its tokens then mostly share a sequence; the backward pass: 87 us against
+// 89), or every n-th item, so that the warps running together read and write
+// neighbouring tokens (the norms: 114 us against 130).
+__device__ __forceinline__ Passes warp_share(int64_t n_work, int64_t i, int64_t n, int splits,
+                                             int groups, bool contiguous) {
+  Passes p;
+  p.w = contiguous ? n_work * i / n : i;
+  p.w_hi = contiguous ? n_work * (i + 1) / n : n_work;
+  p.step = contiguous ? 1 : n;
+  p.t = 0;
+  p.gi = p.g_hi = 0;
+  if (p.more()) p.start(splits, groups);
+  return p;
+}
+
+// A weight into shared memory in fp32 (ones without), by the whole CTA.
+template <typename T, int D>
+__device__ __forceinline__ void stage_weight(const void* w, float* out) {
+  for (int d = threadIdx.x; d < D; d += kNRThreads)
+    out[d] = w ? Elem<T>::to_f(static_cast<const T*>(w)[d]) : 1.f;
+}
+// N pairs from shared memory (16-byte aligned).
+template <int N>
+__device__ __forceinline__ void lds_pairs(const float* p, f2* out) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+    out[i] = v.x;
+    out[i + 1] = v.y;
+  }
 }
 
 struct NRArgs {
@@ -127,115 +259,219 @@ struct NRArgs {
   TurnTab tab;
 };
 
-// Forward.  A warp takes one token and one of `splits` equal parts of its
-// head rows: q heads, then k heads, then (append) v heads.
+// Forward: rows a lane holds in a pass and passes in flight (6 KB a warp
+// either way).  Two rows, two independent chains of arithmetic, serve the
+// append, whose tokens are short and dear to place (22,000 tokens of 16 rows:
+// 52 us with one row, 38 with two); one row serves the norms, which stream
+// better in smaller steps (32,799 tokens of 40 rows: 114 us against 121).
+template <bool kAppend> struct FwdCfg {
+  static constexpr int ROWS = kAppend ? 2 : 1;
+  static constexpr int DEPTH = 6 / ROWS;
+};
+
 template <typename T, int D, bool kAppend>
-__global__ void __launch_bounds__(kNRThreads)
+__global__ void __launch_bounds__(kNRThreads, 2)
 norm_rope_kernel(const __grid_constant__ NRArgs a) {
   using M = RowMap<T, D>;
-  constexpr int HALF = M::HALF, VEC = M::VEC;
-  __shared__ float2 cs_all[kNRWarps][HALF];
+  constexpr int HALF = M::HALF, VEC = M::VEC, NP2 = VEC / 2;
+  constexpr int U = FwdCfg<kAppend>::ROWS, kDepth = FwdCfg<kAppend>::DEPTH;
+  constexpr int GR = M::RPW * U;                     // rows of a pass
+  extern __shared__ __align__(16) uint4 ring_all[];  // [warp][kDepth][U][2][lane]
+  __shared__ __align__(16) float cs_all[kNRWarps][D];
+  __shared__ __align__(16) float wts[2][D];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % M::LPR, sub = lane / M::LPR;
-  float2* cs = cs_all[warp];
-  const int rows = a.Hq + a.H + (kAppend ? a.H : 0);
-  const int groups = (rows + M::RPW - 1) / M::RPW;
-  const int64_t n_work = a.n_tok * a.splits;
-  for (int64_t w = (int64_t)blockIdx.x * kNRWarps + warp; w < n_work;
-       w += (int64_t)gridDim.x * kNRWarps) {
-    const int64_t t = w / a.splits;
-    const int part = (int)(w % a.splits);
-    const int h_lo = (int)((int64_t)part * groups / a.splits) * M::RPW;
-    const int h_hi = min(rows, (int)((int64_t)(part + 1) * groups / a.splits) * M::RPW);
-    int64_t cache_row = -1;  // row 0 of this token's head 0 in the pages, or none
-    if (kAppend) {
-      if (t < a.tok_offsets[0] || t >= a.tok_offsets[a.B]) continue;  // padding token
-      const int64_t b = warp_find_segment(a.tok_offsets, a.B, t);
-      const int64_t slot = (int64_t)a.cache_len[b] + (t - a.tok_offsets[b]);
-      if (slot < 0) {
-        if (lane == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
-      } else if (slot >= (int64_t)a.max_pages * a.page_size) {
-        if (lane == 0) record_error(a.status, MSA_ERR_CAPACITY);
+  float* cs = cs_all[warp];
+  uint4* ring = ring_all + warp * kDepth * U * 64 + lane;
+  const int gq = (a.Hq + GR - 1) / GR, gk = (a.H + GR - 1) / GR;
+  const int groups = gq + gk + (kAppend ? gk : 0);
+  const bool rot = a.positions != nullptr;
+
+  Passes at = warp_share(a.n_tok * a.splits, (int64_t)blockIdx.x * kNRWarps + warp,
+                         (int64_t)gridDim.x * kNRWarps, a.splits, groups,
+                         kAppend && a.splits == 1);
+  Passes ahead = at;
+  auto issue = [&](int slot) {
+    if (ahead.more()) {
+      const T* src;
+      int r = ahead.gi, heads = a.H;
+      if (r < gq) {
+        heads = a.Hq;
+        src = static_cast<const T*>(a.q) + ahead.t * a.q_stride;
+      } else if (!kAppend || r < gq + gk) {
+        r -= gq;
+        src = static_cast<const T*>(a.k) + ahead.t * a.k_stride;
       } else {
-        const int pg = a.block_table[b * a.max_pages + slot / a.page_size];
-        if (pg < 0 || pg >= a.n_pages) {
-          if (lane == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
-        } else {
-          cache_row = (int64_t)pg * a.H * a.page_size + slot % a.page_size;
+        r -= gq + gk;
+        src = static_cast<const T*>(a.v) + ahead.t * a.v_stride;
+      }
+      r = r * GR + sub;
+      src += r * D + l * VEC;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r + u * M::RPW < heads) {
+          uint4* d = ring + (slot * U + u) * 64;
+          cp16(d, src + u * M::RPW * D);
+          cp16(d + 32, src + u * M::RPW * D + HALF);
         }
+      ahead.next(a.splits, groups);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) issue(i);
+
+  stage_weight<T, D>(a.wq, wts[0]);
+  stage_weight<T, D>(a.wk, wts[1]);
+  if (!rot)
+    for (int i = lane; i < D; i += 32) cs[i] = i < HALF ? 1.f : 0.f;
+  __syncthreads();
+  uint64_t freq[HALF / 32];
+#pragma unroll
+  for (int i = 0; i < HALF / 32; ++i) freq[i] = a.tab.f[i * 32 + lane];
+
+  // append: the sequence of the last token, and where this token's rows go:
+  // row 0 of head 0 in the pages, -1: nowhere, -2: padding, nothing is written
+  int64_t seq = -1, seq_lo = 0, seq_hi = -1, cache_row = -1;
+  int seq_len = 0;
+  const int64_t tok_lo = kAppend ? a.tok_offsets[0] : 0;
+  const int64_t tok_hi = kAppend ? a.tok_offsets[a.B] : 0;
+  // y1 = x1 ca + x2 cb, y2 = x2 cc + x1 cd, of x scaled by r: the weight and
+  // the rotation of the token and tensor at hand
+  f2 ca[NP2], cb[NP2], cc[NP2], cd[NP2];
+  bool fresh = true;
+  for (int slot = 0; at.more(); slot = slot + 1 == kDepth ? 0 : slot + 1) {
+    const int64_t t = at.t;
+    const int gi = at.gi;
+    if (fresh) {
+      if (kAppend) {
+        cache_row = -2;
+        if (t >= tok_lo && t < tok_hi) {
+          cache_row = -1;
+          if (t < seq_lo || t >= seq_hi) {
+            seq = warp_find_segment(a.tok_offsets, a.B, t);
+            seq_lo = a.tok_offsets[seq];
+            seq_hi = a.tok_offsets[seq + 1];
+            seq_len = a.cache_len[seq];
+          }
+          const int64_t row = (int64_t)seq_len + (t - seq_lo);
+          if (row < 0) {
+            if (lane == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
+          } else if (row >= (int64_t)a.max_pages * a.page_size) {
+            if (lane == 0) record_error(a.status, MSA_ERR_CAPACITY);
+          } else {
+            const int pi = (int)row / a.page_size;  // row < 2^31: checked by the host
+            const int pg = a.block_table[seq * a.max_pages + pi];
+            if (pg < 0 || pg >= a.n_pages) {
+              if (lane == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
+            } else {
+              cache_row = (int64_t)pg * a.H * a.page_size + ((int)row - pi * a.page_size);
+            }
+          }
+        }
+      }
+      if (rot) token_cs<HALF>(freq, a.positions[t], cs, lane);
+    }
+    const bool isq = gi < gq, isv = kAppend && gi >= gq + gk;
+    const bool weighted = isq ? a.wq != nullptr : a.wk != nullptr;
+    const bool copied = isv || !(weighted || rot);
+    if ((fresh || gi == gq) && !copied) {
+      f2 w1[NP2], w2[NP2], c[NP2], s[NP2];
+      lds_pairs<NP2>(wts[!isq] + l * VEC, w1);
+      lds_pairs<NP2>(wts[!isq] + HALF + l * VEC, w2);
+      lds_pairs<NP2>(cs + l * VEC, c);
+      lds_pairs<NP2>(cs + HALF + l * VEC, s);
+#pragma unroll
+      for (int e = 0; e < NP2; ++e) {
+        ca[e] = mul2(w1[e], c[e]);
+        cb[e] = mul2(w2[e], s[e]) ^ 0x8000000080000000ull;
+        cc[e] = mul2(w2[e], c[e]);
+        cd[e] = mul2(w1[e], s[e]);
       }
     }
-    const bool rot = a.positions != nullptr;
-    float c[VEC], s[VEC];
-    if (rot) {
-      token_cs<HALF>(a.tab, a.positions[t], cs, lane);
+    // this lane's first row: where it is written, the next U - 1 rows dst_step on
+    const int r = (isq ? gi : isv ? gi - gq - gk : gi - gq) * GR + sub;
+    int heads = isq ? a.Hq : a.H;
+    T* dst;
+    int64_t dst_step = M::RPW * D;
+    if (isq) {
+      dst = static_cast<T*>(a.q_out) + (t * a.Hq + r) * D;
+      if (kAppend && cache_row == -2) heads = 0;
+    } else if (!kAppend) {
+      dst = static_cast<T*>(a.k_out) + (t * a.H + r) * D;
+    } else {
+      if (cache_row < 0) heads = 0;
+      dst = static_cast<T*>(isv ? a.v_pages : a.k_pages) +
+            (cache_row + (int64_t)r * a.page_size) * D;
+      dst_step *= a.page_size;
+    }
+    dst += l * VEC;
+    cp_wait<kDepth - 1>();
+    uint4 r1[U], r2[U];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        c[e] = cs[l * VEC + e].x;
-        s[e] = cs[l * VEC + e].y;
+    for (int u = 0; u < U; ++u) {
+      r1[u] = ring[(slot * U + u) * 64];
+      r2[u] = ring[(slot * U + u) * 64 + 32];
+    }
+    if (!copied) {
+      f2 x1[U][NP2], x2[U][NP2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        pairs<T>(r1[u], x1[u]);
+        pairs<T>(r2[u], x2[u]);
+      }
+      if (weighted) {
+        // (lanes without a row sum garbage among themselves)
+        float ss[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          f2 s1 = mul2(x1[u][0], x1[u][0]), s2 = mul2(x2[u][0], x2[u][0]);
+#pragma unroll
+          for (int e = 1; e < NP2; ++e) {
+            s1 = fma2(x1[u][e], x1[u][e], s1);
+            s2 = fma2(x2[u][e], x2[u][e], s2);
+          }
+          ss[u] = (un2(s1).x + un2(s1).y) + (un2(s2).x + un2(s2).y);
+        }
+#pragma unroll
+        for (int o = M::LPR / 2; o; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float rs = rsqrtf(fmaf(ss[u], 1.f / D, a.eps));
+          const f2 rr = mk2(rs, rs);
+#pragma unroll
+          for (int e = 0; e < NP2; ++e) {
+            x1[u][e] = mul2(x1[u][e], rr);
+            x2[u][e] = mul2(x2[u][e], rr);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < NP2; ++e) {
+          const f2 y1 = fma2(x1[u][e], ca[e], mul2(x2[u][e], cb[e]));
+          x2[u][e] = fma2(x2[u][e], cc[e], mul2(x1[u][e], cd[e]));
+          x1[u][e] = y1;
+        }
+        r1[u] = from_pairs<T>(x1[u]);
+        r2[u] = from_pairs<T>(x2[u]);
       }
     }
-    for (int h0 = h_lo; h0 < h_hi; h0 += M::RPW) {
-      const int h = h0 + sub;
-      const bool ok = h < h_hi;
-      const bool isq = h < a.Hq, isv = kAppend && h >= a.Hq + a.H;
-      const T* src = nullptr;
-      T* dst = nullptr;
-      const T* wt = nullptr;
-      if (ok && isq) {
-        src = static_cast<const T*>(a.q) + t * a.q_stride + (int64_t)h * D;
-        dst = static_cast<T*>(a.q_out) + (t * a.Hq + h) * D;
-        wt = static_cast<const T*>(a.wq);
-      } else if (ok) {
-        const int g = isv ? h - a.Hq - a.H : h - a.Hq;
-        src = isv ? static_cast<const T*>(a.v) + t * a.v_stride + (int64_t)g * D
-                  : static_cast<const T*>(a.k) + t * a.k_stride + (int64_t)g * D;
-        wt = isv ? nullptr : static_cast<const T*>(a.wk);
-        if (kAppend) {
-          if (cache_row >= 0)
-            dst = static_cast<T*>(isv ? a.v_pages : a.k_pages) +
-                  (cache_row + (int64_t)g * a.page_size) * D;
-        } else {
-          dst = static_cast<T*>(a.k_out) + (t * a.H + g) * D;
-        }
-      }
-      float x1[VEC], x2[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x1[e] = x2[e] = 0.f;
-      if (dst) {
-        load_f<T, VEC>(src + l * VEC, x1);
-        load_f<T, VEC>(src + HALF + l * VEC, x2);
+    for (int u = 0; u < U; ++u)
+      if (r + u * M::RPW < heads) {
+        st16(dst + u * dst_step, r1[u]);
+        st16(dst + u * dst_step + HALF, r2[u]);
       }
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) ss = fmaf(x1[e], x1[e], fmaf(x2[e], x2[e], ss));
-      ss = row_sum<M::LPR>(ss);
-      if (!dst) continue;
-      if (wt) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float w1[VEC], w2[VEC];
-        load_f<T, VEC>(wt + l * VEC, w1);
-        load_f<T, VEC>(wt + HALF + l * VEC, w2);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          x1[e] *= r * w1[e];
-          x2[e] *= r * w2[e];
-        }
-      }
-      if (rot && !isv) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float y1 = x1[e] * c[e] - x2[e] * s[e];
-          x2[e] = x2[e] * c[e] + x1[e] * s[e];
-          x1[e] = y1;
-        }
-      }
-      store_f<T, VEC>(dst + l * VEC, x1);
-      store_f<T, VEC>(dst + HALF + l * VEC, x2);
-    }
+    issue(slot);  // this lane's reads of the slot have been used
+    fresh = at.next(a.splits, groups);
   }
+  cp_wait<0>();
 }
 
 struct NRBArgs {
@@ -253,115 +489,168 @@ struct NRBArgs {
   TurnTab tab;
 };
 
-// Backward: warps walk the tokens, first over the q heads, then over the k
-// heads, keeping the weight gradient of their lanes' dims in registers; each
-// CTA writes one partial per weight, in fixed order.
+constexpr int kDepthBack = 2;  // backward: passes in flight, 2 or 3 KB each a warp
+
+// Backward: the same walk over x and dy, first of q, then of k; the weight
+// gradient of a lane's dims stays in registers over all its rows, each CTA
+// writes one partial per weight, in a fixed order.
 template <typename T, typename E, int D>
-__global__ void __launch_bounds__(kNRThreads)
+__global__ void __launch_bounds__(kNRThreads, 2)
 norm_rope_backward_kernel(const __grid_constant__ NRBArgs a) {
   using M = RowMap<T, D>;
-  constexpr int HALF = M::HALF, VEC = M::VEC;
-  __shared__ float2 cs_all[kNRWarps][HALF];
+  constexpr int HALF = M::HALF, VEC = M::VEC, EV = VEC / Vec16<E>::N;
+  constexpr int NP2 = VEC / 2, EP = Vec16<E>::N / 2;
+  constexpr int NP = 2 + 2 * EV;                     // 16-byte pieces of a lane and pass
+  extern __shared__ __align__(16) uint4 ring_all[];  // [warp][kDepthBack][NP][lane]
+  __shared__ __align__(16) float cs_all[kNRWarps][D];
+  __shared__ __align__(16) float wts[2][D];
   __shared__ float red[kNRWarps][D];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % M::LPR, sub = lane / M::LPR;
-  float2* cs = cs_all[warp];
+  float* cs = cs_all[warp];
+  uint4* ring = ring_all + warp * kDepthBack * NP * 32 + lane;
   const bool rot = a.positions != nullptr;
+  stage_weight<T, D>(a.wq, wts[0]);
+  stage_weight<T, D>(a.wk, wts[1]);
+  __syncthreads();
+  uint64_t freq[HALF / 32];
+#pragma unroll
+  for (int i = 0; i < HALF / 32; ++i) freq[i] = a.tab.f[i * 32 + lane];
+
   for (int side = 0; side < 2; ++side) {
     const int heads = side ? a.H : a.Hq;
     if (heads == 0) continue;
     const T* x = static_cast<const T*>(side ? a.k : a.q);
     const int64_t xs = side ? a.k_stride : a.q_stride;
-    const T* wt = static_cast<const T*>(side ? a.wk : a.wq);
     const E* dy = static_cast<const E*>(side ? a.dk_out : a.dq_out);
     E* dx = static_cast<E*>(side ? a.dk : a.dq);
     const int64_t ds = side ? a.dk_stride : a.dq_stride;
-    float w1[VEC], w2[VEC], a1[VEC], a2[VEC];
+    const bool weighted = side ? a.wk != nullptr : a.wq != nullptr;
+    const int groups = (heads + M::RPW - 1) / M::RPW;
+    Passes at = warp_share(a.n_tok, (int64_t)blockIdx.x * kNRWarps + warp,
+                           (int64_t)gridDim.x * kNRWarps, 1, groups, true);
+    Passes ahead = at;
+    auto issue = [&](int slot) {
+      if (ahead.more()) {
+        const int r = ahead.gi * M::RPW + sub;
+        if (r < heads) {
+          uint4* d = ring + slot * NP * 32;
+          const E* gp = dy + (ahead.t * heads + r) * D + l * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) a1[e] = a2[e] = 0.f;
-    if (wt) {
-      load_f<T, VEC>(wt + l * VEC, w1);
-      load_f<T, VEC>(wt + HALF + l * VEC, w2);
-    }
-    for (int64_t t = (int64_t)blockIdx.x * kNRWarps + warp; t < a.n_tok;
-         t += (int64_t)gridDim.x * kNRWarps) {
-      float c[VEC], s[VEC];
-      if (rot) {
-        token_cs<HALF>(a.tab, a.positions[t], cs, lane);
+          for (int v = 0; v < EV; ++v) {
+            cp16(d + 32 * (2 + v), gp + v * Vec16<E>::N);
+            cp16(d + 32 * (2 + EV + v), gp + HALF + v * Vec16<E>::N);
+          }
+          if (weighted) {
+            const T* xp = x + ahead.t * xs + r * D + l * VEC;
+            cp16(d, xp);
+            cp16(d + 32, xp + HALF);
+          }
+        }
+        ahead.next(1, groups);
+      }
+      cp_commit();
+    };
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          c[e] = cs[l * VEC + e].x;
-          s[e] = cs[l * VEC + e].y;
+    for (int i = 0; i < kDepthBack; ++i) issue(i);
+
+    f2 a1[NP2], a2[NP2];  // the weight's gradient
+#pragma unroll
+    for (int e = 0; e < NP2; ++e) a1[e] = a2[e] = 0;
+    bool fresh = true;
+    for (int slot = 0; at.more(); slot = slot + 1 == kDepthBack ? 0 : slot + 1) {
+      const int64_t t = at.t;
+      if (fresh && rot) token_cs<HALF>(freq, a.positions[t], cs, lane);
+      const int r = at.gi * M::RPW + sub;
+      const bool ok = r < heads;
+      cp_wait<kDepthBack - 1>();
+      const uint4* d = ring + slot * NP * 32;
+      f2 x1[NP2], x2[NP2], g1[NP2], g2[NP2];
+#pragma unroll
+      for (int v = 0; v < EV; ++v) {
+        pairs<E>(d[32 * (2 + v)], g1 + v * EP);
+        pairs<E>(d[32 * (2 + EV + v)], g2 + v * EP);
+      }
+      pairs<T>(d[0], x1);
+      pairs<T>(d[32], x2);
+      if (!ok) {  // lanes without a row add zeros to the weight's gradient
+#pragma unroll
+        for (int e = 0; e < NP2; ++e) {
+          x1[e] = x2[e] = mk2(1.f, 1.f);
+          g1[e] = g2[e] = 0;
         }
       }
-      for (int h0 = 0; h0 < heads; h0 += M::RPW) {
-        const int h = h0 + sub;
-        const bool ok = h < heads;
-        float x1[VEC], x2[VEC], g1[VEC], g2[VEC];
+      if (rot) {  // dz = R(-p) dy
+        f2 c[NP2], s[NP2];
+        lds_pairs<NP2>(cs + l * VEC, c);
+        lds_pairs<NP2>(cs + HALF + l * VEC, s);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x1[e] = x2[e] = g1[e] = g2[e] = 0.f;
-        if (ok) {
-          const E* gp = dy + (t * heads + h) * D;
-          load_f<E, VEC>(gp + l * VEC, g1);
-          load_f<E, VEC>(gp + HALF + l * VEC, g2);
-          if (wt) {
-            const T* xp = x + t * xs + (int64_t)h * D;
-            load_f<T, VEC>(xp + l * VEC, x1);
-            load_f<T, VEC>(xp + HALF + l * VEC, x2);
-          }
-        }
-        if (rot) {  // dz = R(-p) dy
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float z1 = g1[e] * c[e] + g2[e] * s[e];
-            g2[e] = g2[e] * c[e] - g1[e] * s[e];
-            g1[e] = z1;
-          }
-        }
-        if (wt) {
-          float ss = 0.f, gx = 0.f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            ss = fmaf(x1[e], x1[e], fmaf(x2[e], x2[e], ss));
-            gx = fmaf(g1[e] * w1[e], x1[e], fmaf(g2[e] * w2[e], x2[e], gx));
-          }
-          ss = row_sum<M::LPR>(ss);
-          gx = row_sum<M::LPR>(gx);
-          const float r = ok ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-          const float m = r * r * (gx * (1.f / D));  // r mean(g x r)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            a1[e] = fmaf(g1[e], x1[e] * r, a1[e]);
-            a2[e] = fmaf(g2[e], x2[e] * r, a2[e]);
-            g1[e] = r * (g1[e] * w1[e] - x1[e] * m);
-            g2[e] = r * (g2[e] * w2[e] - x2[e] * m);
-          }
-        }
-        if (ok) {
-          E* op = dx + t * ds + (int64_t)h * D;
-          store_f<E, VEC>(op + l * VEC, g1);
-          store_f<E, VEC>(op + HALF + l * VEC, g2);
+        for (int e = 0; e < NP2; ++e) {
+          const f2 z1 = fma2(g1[e], c[e], mul2(g2[e], s[e]));
+          g2[e] = fma2(g2[e], c[e], mul2(g1[e], s[e]) ^ 0x8000000080000000ull);
+          g1[e] = z1;
         }
       }
+      if (weighted) {
+        f2 w1[NP2], w2[NP2];
+        lds_pairs<NP2>(wts[side] + l * VEC, w1);
+        lds_pairs<NP2>(wts[side] + HALF + l * VEC, w2);
+        f2 s1 = 0, s2 = 0, h1 = 0, h2 = 0;
+#pragma unroll
+        for (int e = 0; e < NP2; ++e) {
+          s1 = fma2(x1[e], x1[e], s1);
+          s2 = fma2(x2[e], x2[e], s2);
+          w1[e] = mul2(g1[e], w1[e]);
+          w2[e] = mul2(g2[e], w2[e]);
+          h1 = fma2(w1[e], x1[e], h1);
+          h2 = fma2(w2[e], x2[e], h2);
+        }
+        float ss = (un2(s1).x + un2(s1).y) + (un2(s2).x + un2(s2).y);
+        float gx = (un2(h1).x + un2(h1).y) + (un2(h2).x + un2(h2).y);
+#pragma unroll
+        for (int o = M::LPR / 2; o; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          gx += __shfl_xor_sync(0xffffffffu, gx, o);
+        }
+        const float rs = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        const float m = -rs * rs * (gx * (1.f / D));  // - r mean(g x r)
+        const f2 rr = mk2(rs, rs), mm = mk2(m, m);
+#pragma unroll
+        for (int e = 0; e < NP2; ++e) {
+          a1[e] = fma2(g1[e], mul2(x1[e], rr), a1[e]);
+          a2[e] = fma2(g2[e], mul2(x2[e], rr), a2[e]);
+          g1[e] = mul2(rr, fma2(x1[e], mm, w1[e]));
+          g2[e] = mul2(rr, fma2(x2[e], mm, w2[e]));
+        }
+      }
+      if (ok) {
+        E* op = dx + t * ds + r * D + l * VEC;
+#pragma unroll
+        for (int v = 0; v < EV; ++v) {
+          st16(op + v * Vec16<E>::N, from_pairs<E>(g1 + v * EP));
+          st16(op + HALF + v * Vec16<E>::N, from_pairs<E>(g2 + v * EP));
+        }
+      }
+      issue(slot);  // this lane's reads of the slot have been used
+      fresh = at.next(1, groups);
     }
-    if (!wt) continue;
+    cp_wait<0>();
+    if (!weighted) continue;
+
     // the warp's rows, then the CTA's warps
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-      for (int o = M::LPR; o < 32; o <<= 1) {
-        a1[e] += __shfl_xor_sync(0xffffffffu, a1[e], o);
-        a2[e] += __shfl_xor_sync(0xffffffffu, a2[e], o);
-      }
-    }
     __syncthreads();  // earlier readers of red are done
-    if (sub == 0) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        red[warp][l * VEC + e] = a1[e];
-        red[warp][HALF + l * VEC + e] = a2[e];
+    for (int e = 0; e < NP2; ++e) {
+      float v[4] = {un2(a1[e]).x, un2(a1[e]).y, un2(a2[e]).x, un2(a2[e]).y};
+#pragma unroll
+      for (int o = M::LPR; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      if (sub == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp][(i >> 1) * HALF + l * VEC + 2 * e + (i & 1)] = v[i];
       }
     }
     __syncthreads();
@@ -374,46 +663,55 @@ norm_rope_backward_kernel(const __grid_constant__ NRBArgs a) {
   }
 }
 
-// Sums the CTAs' partials of one weight (blockIdx.x: 0 = q, 1 = k): 1024 / D
-// threads a dim, each a fixed stride of the CTAs, in double (a few hundred
-// values; the sum is rounded once).
+// Sums the CTAs' partials: block (x, y) 32 dims from 32 x of the weight of q
+// (y = 0) or k, thread (i, d) every 32nd partial; in double, in a fixed order,
+// rounded once.
 template <int D>
 __global__ void __launch_bounds__(1024)
 weight_grad_kernel(int n_part, const float* __restrict__ part, float* __restrict__ dwq,
                    float* __restrict__ dwk) {
-  __shared__ double red[1024];
+  __shared__ double red[32][33];
   pdl_trigger();
   pdl_wait();
-  float* dw = blockIdx.x ? dwk : dwq;
+  float* dw = blockIdx.y ? dwk : dwq;
   if (!dw) return;
-  const int d = threadIdx.x % D, i0 = threadIdx.x / D;
+  const int d = threadIdx.x & 31, i0 = threadIdx.x >> 5;
   double v = 0.0;
-  for (int i = i0; i < n_part; i += 1024 / D)
-    v += (double)part[((int64_t)i * 2 + blockIdx.x) * D + d];
-  red[threadIdx.x] = v;
+#pragma unroll 4
+  for (int i = i0; i < n_part; i += 32)
+    v += (double)part[((int64_t)i * 2 + blockIdx.y) * D + blockIdx.x * 32 + d];
+  red[i0][d] = v;
   __syncthreads();
-  if (i0 == 0) {
-    for (int i = 1; i < 1024 / D; ++i) v += red[i * D + d];
-    dw[d] = (float)v;
-  }
+  // warp i0 joins dim i0's 32 sums
+  v = red[d][i0];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (d == 0) dw[blockIdx.x * 32 + i0] = (float)v;
 }
 
-// Parts a token's head rows are cut into: one warp a token once there are
-// about 16 warps an SM, else parts of at least one warp-load of rows, so a
-// short call still reaches every SM.
-int head_splits(int64_t n_tok, int rows, int rpw) {
-  const int64_t want = 16LL * num_sms();
-  const int64_t s = (want + n_tok - 1) / n_tok;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(s, (rows + rpw - 1) / rpw));
+// Parts a token's row groups are cut into: whole tokens once a resident warp
+// has four or more of them, else so many parts that there are about four a
+// warp (the shares are then even, and a short call reaches every SM).
+int head_splits(int64_t n_tok, int groups, int64_t warps) {
+  const int64_t s = (4 * warps + n_tok - 1) / n_tok;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(s, groups));
 }
+
+constexpr int kCtasFwd = 2, kCtasBack = 2;  // resident on an SM
 
 template <typename T, int D, bool kAppend>
 int launch_forward(NRArgs a, cudaStream_t s) {
-  const int rows = a.Hq + a.H + (kAppend ? a.H : 0);
-  a.splits = head_splits(a.n_tok, rows, RowMap<T, D>::RPW);
-  const int64_t ctas = (a.n_tok * a.splits + kNRWarps - 1) / kNRWarps;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, 1 << 20);
-  return launch_pdl(norm_rope_kernel<T, D, kAppend>, dim3(grid), dim3(kNRThreads), 0, s, a);
+  using M = RowMap<T, D>;
+  using F = FwdCfg<kAppend>;
+  constexpr int GR = M::RPW * F::ROWS;
+  const int gq = (a.Hq + GR - 1) / GR, gk = (a.H + GR - 1) / GR;
+  const int64_t ctas = (int64_t)kCtasFwd * num_sms();
+  a.splits = head_splits(a.n_tok, gq + gk * (kAppend ? 2 : 1), ctas * kNRWarps);
+  const int64_t need = (a.n_tok * a.splits + kNRWarps - 1) / kNRWarps;
+  constexpr int kSmem = kNRWarps * F::DEPTH * F::ROWS * 64 * 16;
+  auto kern = norm_rope_kernel<T, D, kAppend>;
+  if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmem)) return rc;
+  return launch_pdl(kern, dim3((unsigned)std::min(ctas, need)), dim3(kNRThreads), kSmem, s, a);
 }
 
 template <bool kAppend>
@@ -427,17 +725,18 @@ int dispatch_forward(msa_dtype dt, int D, const NRArgs& a, cudaStream_t s) {
 
 int backward_grid(int64_t n_tok) {
   const int64_t ctas = (n_tok + kNRWarps - 1) / kNRWarps;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, 2LL * num_sms()));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)kCtasBack * num_sms()));
 }
 
 template <typename T, typename E, int D>
 int launch_backward(const NRBArgs& a, float* dwq, float* dwk, cudaStream_t s) {
   const int grid = backward_grid(a.n_tok);
-  if (int rc = launch_pdl(norm_rope_backward_kernel<T, E, D>, dim3(grid), dim3(kNRThreads), 0, s,
-                          a))
-    return rc;
+  constexpr int kSmem = kNRWarps * kDepthBack * (2 + 2 * (RowMap<T, D>::VEC / Vec16<E>::N)) * 512;
+  auto kern = norm_rope_backward_kernel<T, E, D>;
+  if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmem)) return rc;
+  if (int rc = launch_pdl(kern, dim3(grid), dim3(kNRThreads), kSmem, s, a)) return rc;
   if (!dwq && !dwk) return MSA_OK;
-  return launch_pdl(weight_grad_kernel<D>, dim3(2), dim3(1024), 0, s, grid,
+  return launch_pdl(weight_grad_kernel<D>, dim3(D / 32, 2), dim3(1024), 0, s, grid,
                     static_cast<const float*>(a.part), dwq, dwk);
 }
 

@@ -132,17 +132,29 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_torch = None
+
+
+def _th():
+    """torch, imported with the first call that needs it (the checks below run
+    several times a call, and a small call's time is theirs)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _th().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def dtype_code(t) -> int:
-    import torch
+    torch = _th()
     if t == torch.float32:
         return MSA_F32
     if t == torch.bfloat16:
@@ -163,10 +175,15 @@ def _check(name: str, rc: int):
 F32, I32, I64 = "f32", "i32", "i64"
 
 
+_DTYPES: dict = {}
+
+
 def _torch_dtype(kind):
-    import torch
-    return {MSA_F32: torch.float32, MSA_BF16: torch.bfloat16, F32: torch.float32,
-            I32: torch.int32, I64: torch.int64}.get(kind)
+    if not _DTYPES:
+        torch = _th()
+        _DTYPES.update({MSA_F32: torch.float32, MSA_BF16: torch.bfloat16, F32: torch.float32,
+                        I32: torch.int32, I64: torch.int64})
+    return _DTYPES.get(kind)
 
 
 def _es(dt):
@@ -178,9 +195,8 @@ def _es(dt):
 def _device_ok(t, host_ok: bool) -> bool:
     """A tensor the kernels may read: on the current CUDA device, or (where
     the call reads a tiered bank over the host link) in pinned host memory."""
-    import torch
-    if t.is_cuda:
-        return t.device.index == torch.cuda.current_device()
+    if t.is_cuda:  # CUDA is up then: its current device without the checks for that
+        return t.get_device() == _th()._C._cuda_getDevice()
     return host_ok and t.is_pinned()
 
 
@@ -206,28 +222,42 @@ def _numel_ok(t, n, what, kind=None, host_ok=False):
                          f"the kernels read it from {where}")
 
 
+def _arg(t, n, what, kind):
+    """The address of a tensor argument that passes _numel_ok."""
+    if t is None or isinstance(t, int):
+        return t
+    if (t.dtype is not _torch_dtype(kind) or t.numel() < n or not t.is_contiguous()
+            or not _device_ok(t, False)):
+        _numel_ok(t, n, what, kind)  # says what is wrong with it
+    return t.data_ptr()
+
+
 def _rows_ok(t, n, heads, D, what, kind) -> int:
     """Checks an operand of n tokens of [heads][D] whose tokens may lie apart
     (a slice of a fused projection's output): each token's heads contiguous,
     the tokens a fixed, 16-byte multiple of elements apart.  Returns that
     stride (heads * D for a raw address, None or an empty tensor)."""
-    dense = heads * D
     if t is None or isinstance(t, int):
-        return dense
+        return heads * D
     want = _torch_dtype(kind)
     if want is not None and t.dtype != want:
         raise ValueError(f"{what} is {t.dtype}, the call reads {want}")
-    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, needs [>= {n}, {heads}, {D}]")
-    if t.shape[0] > 0 and heads > 0:
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < n or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{what} has shape {tuple(shape)}, needs [>= {n}, {heads}, {D}]")
+    stride = heads * D
+    if shape[0] > 0 and heads > 0:
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (heads > 1 and s1 != D):
             raise ValueError(f"{what}: a token's heads must be contiguous")
-        if t.shape[0] > 1 and (t.stride(0) < dense or t.stride(0) * t.element_size() % 16):
-            raise ValueError(f"{what}: tokens must be a multiple of 16 bytes apart, and not "
-                             f"overlap (stride {t.stride(0)} elements)")
+        if shape[0] > 1:
+            if s0 < stride or s0 * t.element_size() % 16:
+                raise ValueError(f"{what}: tokens must be a multiple of 16 bytes apart, and not "
+                                 f"overlap (stride {s0} elements)")
+            stride = s0
     if not _device_ok(t, False):
         raise ValueError(f"{what} is on {t.device}; it must be on the current CUDA device")
-    return t.stride(0) if t.shape[0] > 1 else dense
+    return stride
 
 
 def _ws_ok(ws, ws_bytes):
@@ -484,16 +514,14 @@ def msa_qk_norm_rope(dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, e
                      q_out, k_out, stream=None):
     """q and k: [n_tok][heads][D] tensors, the token strides taken from them
     (raw addresses are dense)."""
-    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
-    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
-    _numel_ok(q_weight, D, "q_weight", _es(dt))
-    _numel_ok(k_weight, D, "k_weight", _es(dt))
-    _numel_ok(positions, n_tok, "positions", I32)
-    _numel_ok(q_out, n_tok * Hq * D, "q_out", _es(dt))
-    _numel_ok(k_out, n_tok * H * D, "k_out", _es(dt))
+    es = _es(dt)
+    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
+    ks = _rows_ok(k, n_tok, H, D, "k", es)
     _check("msa_qk_norm_rope", lib().msa_qk_norm_rope(
-        dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
-        _ptr(positions), eps, rope_base, _ptr(q_out), _ptr(k_out), _stream(stream)))
+        dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _arg(q_weight, D, "q_weight", es),
+        _arg(k_weight, D, "k_weight", es), _arg(positions, n_tok, "positions", I32), eps,
+        rope_base, _arg(q_out, n_tok * Hq * D, "q_out", es),
+        _arg(k_out, n_tok * H * D, "k_out", es), _stream(stream)))
 
 
 def msa_qk_norm_rope_backward_workspace_size(n_tok, D) -> int:
@@ -505,22 +533,19 @@ def msa_qk_norm_rope_backward(dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_we
                               ws_bytes, stream=None):
     """q, k, dq and dk: [n_tok][heads][D] tensors, the token strides taken
     from them (raw addresses are dense)."""
-    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
-    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
-    dqs = _rows_ok(dq, n_tok, Hq, D, "dq", _es(grad_dt))
-    dks = _rows_ok(dk, n_tok, H, D, "dk", _es(grad_dt))
-    _numel_ok(q_weight, D, "q_weight", _es(dt))
-    _numel_ok(k_weight, D, "k_weight", _es(dt))
-    _numel_ok(positions, n_tok, "positions", I32)
-    _numel_ok(dq_out, n_tok * Hq * D, "dq_out", _es(grad_dt))
-    _numel_ok(dk_out, n_tok * H * D, "dk_out", _es(grad_dt))
-    _numel_ok(dq_weight, D, "dq_weight", F32)
-    _numel_ok(dk_weight, D, "dk_weight", F32)
+    es, gs = _es(dt), _es(grad_dt)
+    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
+    ks = _rows_ok(k, n_tok, H, D, "k", es)
+    dqs = _rows_ok(dq, n_tok, Hq, D, "dq", gs)
+    dks = _rows_ok(dk, n_tok, H, D, "dk", gs)
     _ws_ok(ws, ws_bytes)
     _check("msa_qk_norm_rope_backward", lib().msa_qk_norm_rope_backward(
-        dt, grad_dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
-        _ptr(positions), eps, rope_base, _ptr(dq_out), _ptr(dk_out), _ptr(dq), dqs, _ptr(dk), dks,
-        _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws_bytes, _stream(stream)))
+        dt, grad_dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks,
+        _arg(q_weight, D, "q_weight", es), _arg(k_weight, D, "k_weight", es),
+        _arg(positions, n_tok, "positions", I32), eps, rope_base,
+        _arg(dq_out, n_tok * Hq * D, "dq_out", gs), _arg(dk_out, n_tok * H * D, "dk_out", gs),
+        _ptr(dq), dqs, _ptr(dk), dks, _arg(dq_weight, D, "dq_weight", F32),
+        _arg(dk_weight, D, "dk_weight", F32), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_offsets, positions,
@@ -528,23 +553,19 @@ def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_of
                      k_pages, v_pages, q_out, stream=None):
     """q, k and v: [n_tok][heads][D] tensors, the token strides taken from
     them (raw addresses are dense)."""
-    qs = _rows_ok(q, n_tok, Hq, D, "q", _es(dt))
-    ks = _rows_ok(k, n_tok, H, D, "k", _es(dt))
-    vs = _rows_ok(v, n_tok, H, D, "v", _es(dt))
-    _numel_ok(q_weight, D, "q_weight", _es(dt))
-    _numel_ok(k_weight, D, "k_weight", _es(dt))
-    _numel_ok(tok_offsets, B + 1, "tok_offsets", I64)
-    _numel_ok(positions, n_tok, "positions", I32)
-    _numel_ok(block_table, B * max_pages, "block_table", I32)
-    _numel_ok(cache_len, B, "cache_len", I32)
-    _numel_ok(k_pages, n_pages * H * page_size * D, "k_pages", _es(dt))
-    _numel_ok(v_pages, n_pages * H * page_size * D, "v_pages", _es(dt))
-    _numel_ok(q_out, n_tok * Hq * D, "q_out", _es(dt))
+    es = _es(dt)
+    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
+    ks = _rows_ok(k, n_tok, H, D, "k", es)
+    vs = _rows_ok(v, n_tok, H, D, "v", es)
+    pool = n_pages * H * page_size * D
     _check("msa_paged_append", lib().msa_paged_append(
-        dt, B, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
-        _ptr(k_weight), _ptr(tok_offsets), _ptr(positions), eps, rope_base, _ptr(block_table),
-        max_pages, _ptr(cache_len), page_size, n_pages, _ptr(k_pages), _ptr(v_pages),
-        _ptr(q_out), _stream(stream)))
+        dt, B, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+        _arg(q_weight, D, "q_weight", es), _arg(k_weight, D, "k_weight", es),
+        _arg(tok_offsets, B + 1, "tok_offsets", I64), _arg(positions, n_tok, "positions", I32),
+        eps, rope_base, _arg(block_table, B * max_pages, "block_table", I32), max_pages,
+        _arg(cache_len, B, "cache_len", I32), page_size, n_pages,
+        _arg(k_pages, pool, "k_pages", es), _arg(v_pages, pool, "v_pages", es),
+        _arg(q_out, n_tok * Hq * D, "q_out", es), _stream(stream)))
 
 
 def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size) -> int:
@@ -554,20 +575,15 @@ def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_
 def msa_tree_attn(dt, B, n_tok, n_max, Hq, H, D, q, tok_offsets, parents, k_mem, v_mem, mem_len,
                   m_cap, k_pages, v_pages, n_pages, page_size, block_table, max_pages, cache_len,
                   scale, out, ws, ws_bytes, stream=None):
-    _numel_ok(q, n_tok * Hq * D, "q", _es(dt))
-    _numel_ok(tok_offsets, B + 1, "tok_offsets", I64)
-    _numel_ok(parents, n_tok, "parents", I32)
-    _numel_ok(k_mem, B * m_cap * H * D, "k_mem", _es(dt))
-    _numel_ok(v_mem, B * m_cap * H * D, "v_mem", _es(dt))
-    _numel_ok(mem_len, B if m_cap else 0, "mem_len", I32)
-    _numel_ok(k_pages, n_pages * H * page_size * D, "k_pages", _es(dt))
-    _numel_ok(v_pages, n_pages * H * page_size * D, "v_pages", _es(dt))
-    _numel_ok(block_table, B * max_pages, "block_table", I32)
-    _numel_ok(cache_len, B, "cache_len", I32)
-    _numel_ok(out, n_tok * Hq * D, "out", _es(dt))
+    es = _es(dt)
+    rows, mem, pool = n_tok * Hq * D, B * m_cap * H * D, n_pages * H * page_size * D
     _ws_ok(ws, ws_bytes)
     _check("msa_tree_attn", lib().msa_tree_attn(
-        dt, B, n_tok, n_max, Hq, H, D, _ptr(q), _ptr(tok_offsets), _ptr(parents), _ptr(k_mem),
-        _ptr(v_mem), _ptr(mem_len), m_cap, _ptr(k_pages), _ptr(v_pages), n_pages, page_size,
-        _ptr(block_table), max_pages, _ptr(cache_len), scale, _ptr(out), _ptr(ws), ws_bytes,
-        _stream(stream)))
+        dt, B, n_tok, n_max, Hq, H, D, _arg(q, rows, "q", es),
+        _arg(tok_offsets, B + 1, "tok_offsets", I64), _arg(parents, n_tok, "parents", I32),
+        _arg(k_mem, mem, "k_mem", es), _arg(v_mem, mem, "v_mem", es),
+        _arg(mem_len, B if m_cap else 0, "mem_len", I32), m_cap,
+        _arg(k_pages, pool, "k_pages", es), _arg(v_pages, pool, "v_pages", es), n_pages,
+        page_size, _arg(block_table, B * max_pages, "block_table", I32), max_pages,
+        _arg(cache_len, B, "cache_len", I32), scale, _arg(out, rows, "out", es), _ptr(ws),
+        ws_bytes, _stream(stream)))

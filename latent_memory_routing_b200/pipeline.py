@@ -6,8 +6,6 @@ into libmsa.
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import msa as _m
@@ -323,14 +321,25 @@ class Pipeline:
         return self.out
 
 
-def _on(stream):
-    """Tensors made in this context belong to the stream the call runs on (an
-    int is a raw handle), so their memory is not handed on while it runs."""
+def _made(stream, make):
+    """make() with its tensors belonging to the stream the call runs on (an
+    int is a raw handle), so that their memory is not handed on while it
+    runs."""
     if stream is None:
-        return contextlib.nullcontext()
+        return make()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _heads(t):
+    return 0 if t is None else t.shape[1]
+
+
+def _dense(t):
+    """An uninitialised contiguous tensor like t (None for None)."""
+    return None if t is None else t.new_empty(t.shape)
 
 
 def qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -342,12 +351,9 @@ def qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float 
     outputs are contiguous.  ``out`` = (q_out, k_out) to reuse; returns them."""
     x = q if q is not None else k
     n, _, D = x.shape
-    Hq, H = (0 if t is None else t.shape[1] for t in (q, k))
     if out is None:
-        with _on(stream):
-            out = tuple(None if t is None else torch.empty((n, t.shape[1], D), dtype=t.dtype,
-                                                           device=t.device) for t in (q, k))
-    _m.msa_qk_norm_rope(dt_code(x), n, Hq, H, D, q, k, q_weight, k_weight, positions, eps,
+        out = _made(stream, lambda: (_dense(q), _dense(k)))
+    _m.msa_qk_norm_rope(dt_code(x), n, _heads(q), _heads(k), D, q, k, q_weight, k_weight, positions, eps,
                         rope_base, *out, stream)
     return out
 
@@ -370,17 +376,16 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     ``ws``: from qk_norm_rope_backward_workspace (made here if None)."""
     x, dy = (q, dq_out) if q is not None else (k, dk_out)
     n, _, D = x.shape
-    Hq, H = (0 if t is None else t.shape[1] for t in (q, k))
-    with _on(stream):
-        if ws is None:
-            ws = qk_norm_rope_backward_workspace(q, k)
-        if out is None:
-            out = tuple(None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                        for t in (dq_out, dk_out))
-            out += tuple(None if t is None or w is None else
-                         torch.empty(D, dtype=torch.float32, device=t.device)
-                         for t, w in ((q, q_weight), (k, k_weight)))
-    _m.msa_qk_norm_rope_backward(dt_code(x), dt_code(dy), n, Hq, H, D, q, k, q_weight, k_weight,
+
+    def grad(t, w):
+        return None if t is None or w is None else t.new_empty(D, dtype=torch.float32)
+
+    if ws is None:
+        ws = _made(stream, lambda: qk_norm_rope_backward_workspace(q, k))
+    if out is None:
+        out = _made(stream, lambda: (_dense(dq_out), _dense(dk_out), grad(q, q_weight),
+                                     grad(k, k_weight)))
+    _m.msa_qk_norm_rope_backward(dt_code(x), dt_code(dy), n, _heads(q), _heads(k), D, q, k, q_weight, k_weight,
                                  positions, eps, rope_base, dq_out, dk_out, *out, ws,
                                  0 if ws is None else ws.numel(), stream)
     return out
@@ -431,11 +436,9 @@ class PagedCache:
         queries ``q`` [N][Hq][D], norms and rotates them in the same launch
         and returns them (``q_out``, made here if None)."""
         n = k.shape[0]
-        Hq = 0 if q is None else q.shape[1]
         if q is not None and q_out is None:
-            with _on(stream):
-                q_out = torch.empty((n, Hq, self.D), dtype=q.dtype, device=q.device)
-        _m.msa_paged_append(dt_code(k), self.B, n, Hq, self.H, self.D, q, k, v, q_weight,
+            q_out = _made(stream, lambda: _dense(q))
+        _m.msa_paged_append(dt_code(k), self.B, n, _heads(q), self.H, self.D, q, k, v, q_weight,
                             k_weight, tok_offsets, positions, eps, rope_base, self.block_table,
                             self.max_pages, self.cache_len, self.page_size, self.n_pages,
                             self.k_pages, self.v_pages, q_out, stream)
@@ -460,8 +463,7 @@ class TreeAttention:
             raise ValueError(f"the cache holds {cache.B} x {cache.H} x {cache.D}, "
                              f"the attention was made for {B} x {H} x {D}")
         if out is None:
-            with _on(stream):
-                out = torch.empty_like(q)
+            out = _made(stream, lambda: _dense(q))
         _m.msa_tree_attn(self.dt, B, q.shape[0], n_max, Hq, H, D, q, tok_offsets, parents, k_mem,
                          v_mem, mem_len, m_cap, cache.k_pages, cache.v_pages, cache.n_pages,
                          cache.page_size, cache.block_table, cache.max_pages, cache.cache_len,
