@@ -292,9 +292,13 @@ int tree_body(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int 
   a.out = out;
   a.status = device_status_ptr();
   const TreePlan p = tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size);
-  const size_t need = dt == MSA_BF16 ? tree_tc_workspace_size(n_max, a.G, D) : p.total;
+  const bool few = tree_few_takes(n_max, a.G);
+  const size_t need = dt == MSA_F32 ? p.total
+                      : few         ? tree_few_workspace_size(n_max, a.G, D)
+                                    : tree_tc_workspace_size(n_max, a.G, D);
   if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MSA_ERR_WORKSPACE;
-  if (dt == MSA_BF16) return tree_tc_launch(a, D, ws, s);
+  if (dt == MSA_BF16)
+    return few ? tree_few_launch(a, D, ws, s) : tree_tc_launch(a, D, ws, s);
   return D == 64 ? launch_simt<float, 64>(a, p, ws, s) : launch_simt<float, 128>(a, p, ws, s);
 }
 
@@ -305,7 +309,9 @@ extern "C" size_t msa_tree_attn_workspace_size(msa_dtype dt, int B, int n_max, i
                                                int D, int m_cap, int max_pages, int page_size) {
   using namespace msa;
   if (tree_shape(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size)) return 0;
-  if (dt == MSA_BF16) return tree_tc_workspace_size(n_max, Hq / H, D);
+  if (dt == MSA_BF16)
+    return tree_few_takes(n_max, Hq / H) ? tree_few_workspace_size(n_max, Hq / H, D)
+                                         : tree_tc_workspace_size(n_max, Hq / H, D);
   return tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size).total;
 }
 

@@ -132,8 +132,32 @@ __device__ __forceinline__ bool tree_bit(const uint4& m, int j) {
   return (w >> (j & 31)) & 1;
 }
 
-// bf16 on the tensor cores (tree_attn_tc.cu): any shape the entry point
-// takes.  The workspace depends on n_max, G = Hq / H and D.
+// A bf16 pair with its non-finite halves (exponent all ones) replaced by 0.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+// What the merge of partials needs of an item whose first border between two
+// workers' ranges lies at this worker's start: the parts are (worker - 1,
+// slot 1) and (worker .. last, slot 0), rows [row0, row0 + rows) of the item.
+struct TreeCut {
+  int64_t t0;               // the sequence's first token
+  int g, row0, rows, last;  // last < 0: nothing to merge here
+};
+
+// Merges bf16 partials in a fixed order (tree_attn_merge.cu): part (worker,
+// slot) holds part_rows rows of fp32 O and (max, sum) in the base-2 domain.
+int tree_merge_launch(const TreeArgs& a, int D, int workers, int part_rows, const float* part_o,
+                      const float2* part_ml, const TreeCut* cuts, cudaStream_t s);
+
+// bf16, n_max G <= 32 rows a KV head: a warp a worker (tree_attn_few.cu).
+bool tree_few_takes(int n_max, int G);
+size_t tree_few_workspace_size(int n_max, int G, int D);
+int tree_few_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);
+
+// bf16 on tcgen05 (tree_attn_tc.cu): any shape the entry point takes.
 size_t tree_tc_workspace_size(int n_max, int G, int D);
 int tree_tc_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);
 

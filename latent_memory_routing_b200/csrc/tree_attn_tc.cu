@@ -74,13 +74,6 @@ struct ItemE {
   int part;               // partial slot, -1: the whole item, written directly
 };
 
-// What the merging launch needs of the item whose first border lies at a
-// CTA's range start: parts (cta - 1, slot 1), (cta .. last, slot 0).
-struct CutE {
-  int64_t t0;
-  int g, row0, rows, last;  // last < 0: nothing to merge here
-};
-
 struct Aux {
   uint64_t kfull[kMaxSt], kfree[kMaxSt], vfull[kMaxSt], vfree[kMaxSt];
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_empty[2], ml_full;
@@ -129,13 +122,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// A bf16 pair with its non-finite halves (exponent all ones) replaced by 0.
-__device__ __forceinline__ uint32_t finite2(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-  return w;
-}
-
 using u128 = unsigned __int128;
 __device__ __forceinline__ u128 low_bits(int n) {  // bits 0 .. n-1
   return n <= 0 ? (u128)0 : n >= 128 ? ~(u128)0 : (((u128)1 << n) - 1);
@@ -152,7 +138,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
                const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                const __grid_constant__ TreeArgs a, int part_rows, int q_rows, int n_k,
                int n_v, float* __restrict__ part_o, float2* __restrict__ part_ml,
-               CutE* __restrict__ cuts) {
+               TreeCut* __restrict__ cuts) {
   using C = TC<D>;
   constexpr int KB = C::KB;
   constexpr int kBlkRows = 128 * kQT;
@@ -273,7 +259,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
         nt = seq_tiles(s);
         nblk = (s.n * G + kBlkRows - 1) / kBlkRows;
       };
-      CutE cut{0, 0, 0, 0, -1};
+      TreeCut cut{0, 0, 0, 0, -1};
       if (left > 0) {
         b = aux.start_b;
         load_seq();
@@ -615,7 +601,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
                     reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4));
                 const uint4 x = *p;
                 const uint4 y =
-                    make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+                    make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
                 if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
                   *p = y;
                   bad = true;
@@ -826,82 +812,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
   }
 }
 
-// Merges the parts of the items cut by range borders.  blockIdx.x: the border
-// before that CTA's range; blockIdx.y: kRowsBlk rows of the item.  Four warps:
-// one row each (many rows), or one row between them, each a quarter of the
-// parts (few rows: the parts' loads then overlap).
-template <int D, bool kFewRows>
-__global__ void __launch_bounds__(128)
-tree_merge_kernel(const __grid_constant__ TreeArgs a, int part_rows,
-                  const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                  const CutE* __restrict__ cuts) {
-  constexpr int VEC = D / 32;
-  __shared__ float so[4][D];
-  __shared__ float2 sml[4];
-  pdl_trigger();
-  pdl_wait();
-  const CutE cut = cuts[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = kFewRows ? blockIdx.y : blockIdx.y * 4 + warp;
-  if (cut.last < 0 || rr >= cut.rows) return;
-  const int n_parts = cut.last - (int)blockIdx.x + 2;
-  float m = -INFINITY, l = 0.f, o[VEC];
-#pragma unroll
-  for (int x = 0; x < VEC; ++x) o[x] = 0.f;
-  // part 0 is slot 1 of the CTA before the border, part i slot 0 of the
-  // i - 1st after it
-  auto prow = [&](int i) {
-    const int64_t cta = (int64_t)blockIdx.x - 1 + i;
-    return (cta * 2 + (i == 0 ? 1 : 0)) * part_rows + rr;
-  };
-  auto join = [&](float2 ml, const float* v) {
-    if (ml.y == 0.f) return;
-    const float mn = fmaxf(m, ml.x);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float c0 = exp2f(m - ref), c1 = ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref);
-    l = (l == 0.f ? 0.f : l * c0) + ml.y * c1;
-#pragma unroll
-    for (int x = 0; x < VEC; ++x) o[x] = o[x] * c0 + v[x] * c1;
-    m = mn;
-  };
-  const int step = kFewRows ? 4 : 1;
-  for (int i = kFewRows ? warp : 0; i < n_parts; i += 4 * step) {
-    float2 ml[4];
-    float v[4][VEC];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int p = i + x * step;
-      ml[x] = make_float2(-INFINITY, 0.f);
-      if (p < n_parts) {
-        const int64_t pr = prow(p);
-        ml[x] = part_ml[pr];
-        const float* src = part_o + pr * D + lane * VEC;
-#pragma unroll
-        for (int y = 0; y < VEC; ++y) v[x][y] = src[y];
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) join(ml[x], v[x]);
-  }
-  if (kFewRows) {
-    if (lane == 0) sml[warp] = make_float2(m, l);
-#pragma unroll
-    for (int x = 0; x < VEC; ++x) so[warp][lane * VEC + x] = o[x];
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) join(sml[i], &so[i][lane * VEC]);
-  }
-  const int row = cut.row0 + rr;
-  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
-                      ((cut.t0 + row / a.G) * a.Hq + cut.g * a.G + row % a.G) * D + lane * VEC;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int x = 0; x < VEC; x += 2)
-    *reinterpret_cast<uint32_t*>(op + x) =
-        l == 0.f ? 0u : pack2(o[x] * inv, o[x + 1] * inv);
-}
-
 struct TcPlan {
   int qt;          // Q tiles of an item
   int part_rows;   // rows of a partial
@@ -928,7 +838,7 @@ TcPlan tc_plan(int n_max, int G, int D) {
   const size_t parts = 2 * (size_t)num_sms() * p.part_rows;
   p.po_bytes = round_up(parts * D * sizeof(float), 256);
   p.ml_bytes = round_up(parts * sizeof(float2), 256);
-  p.cut_bytes = round_up((size_t)num_sms() * sizeof(CutE), 256);
+  p.cut_bytes = round_up((size_t)num_sms() * sizeof(TreeCut), 256);
   p.total = p.po_bytes + p.ml_bytes + p.cut_bytes;
   return p;
 }
@@ -938,7 +848,7 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   unsigned char* w = static_cast<unsigned char*>(ws);
   float* part_o = reinterpret_cast<float*>(w);
   float2* part_ml = reinterpret_cast<float2*>(w + p.po_bytes);
-  CutE* cuts = reinterpret_cast<CutE*>(w + p.po_bytes + p.ml_bytes);
+  TreeCut* cuts = reinterpret_cast<TreeCut*>(w + p.po_bytes + p.ml_bytes);
   CUtensorMap km, vm, kp, vp;
   const int64_t page_rows = (int64_t)a.n_pages * a.H * a.page_size;
   bool ok = tma_map_sw128_bf16(&kp, a.k_pages, D, 1, page_rows, 1, a.page_size) &&
@@ -955,12 +865,7 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, km, vm, kp, vp, a,
                           p.part_rows, p.q_rows, p.n_k, p.n_v, part_o, part_ml, cuts))
     return rc;
-  // up to 16 rows: a block a row (a decode step's parts are many and short)
-  if (p.part_rows <= 16)
-    return launch_pdl(tree_merge_kernel<D, true>, dim3(grid, (unsigned)p.part_rows), dim3(128), 0,
-                      s, a, p.part_rows, part_o, part_ml, cuts);
-  return launch_pdl(tree_merge_kernel<D, false>, dim3(grid, (unsigned)((p.part_rows + 3) / 4)),
-                    dim3(128), 0, s, a, p.part_rows, part_o, part_ml, cuts);
+  return tree_merge_launch(a, D, (int)grid, p.part_rows, part_o, part_ml, cuts, s);
 }
 
 }  // namespace

@@ -377,7 +377,8 @@ def run_tree(case, n_max, scale=0.0, **kw):
     return out
 
 
-def check_tree(case, out, scale=0.0):
+def expected(case, scale=0.0):
+    """The oracle's output and the bound on an output's distance from it."""
     c, q, off, parents, km, vm, ml, m_cap = case
     o = off.cpu().numpy()
     par = None if parents is None else parents.cpu().numpy()
@@ -390,6 +391,12 @@ def check_tree(case, out, scale=0.0):
     tol = bound * U * (2 * (D + 4) * top[..., None] + 2 * keys + 64)
     if q.dtype == BF16:
         tol = tol + BF * bound + BF * np.abs(want)
+    return want, tol
+
+
+def check_tree(case, out, scale=0.0):
+    o = case[2].cpu().numpy()
+    want, tol = expected(case, scale)
     live = slice(int(o[0]), int(o[-1]))
     close(out[live], want[live], tol[live])
     # rows of no sequence are left as they were
@@ -518,10 +525,14 @@ def test_bad_arrays_are_recorded(dt):
     run_tree(t, 6)
     status(-3)
     t = fresh()
-    t[2][2] = 99                                  # offsets past the tokens
+    exact, tol = expected(t)
+    t[2][2] = 99                                  # offsets past the tokens: skipped
     out = run_tree(t, 6)
     status(-1)
-    assert torch.equal(out[:4], want[:4]) and bool(out[4:].isnan().all())
+    # the sequence that is left is cut into other parts, whose joining rounds
+    # otherwise: each result keeps the formula's bound, not the other's bits
+    close(out[:4], exact[:4], tol[:4])
+    assert bool(out[4:].isnan().all())
 
 
 @pytest.mark.parametrize("case", [TREES[0], TREES[5], TREES[4], TREES[11]],
