@@ -147,10 +147,12 @@ struct TreeCut {
   int g, row0, rows, last;  // last < 0: nothing to merge here
 };
 
-// Merges bf16 partials in a fixed order (tree_attn_merge.cu): part (worker,
-// slot) holds part_rows rows of fp32 O and (max, sum) in the base-2 domain.
-int tree_merge_launch(const TreeArgs& a, int D, int workers, int part_rows, const float* part_o,
-                      const float2* part_ml, const TreeCut* cuts, cudaStream_t s);
+// Merges the bf16 partials of ctas x per workers (per <= 32) in a fixed order
+// (tree_attn_merge.cu): part (worker, slot) holds part_rows rows of fp32 O and
+// (max, sum) in the base-2 domain.
+int tree_merge_launch(const TreeArgs& a, int D, int ctas, int per, int part_rows,
+                      const float* part_o, const float2* part_ml, const TreeCut* cuts,
+                      cudaStream_t s);
 
 // bf16, n_max G <= 32 rows a KV head: a warp a worker (tree_attn_few.cu).
 bool tree_few_takes(int n_max, int G);

@@ -38,7 +38,7 @@ namespace {
 constexpr int kSlice = 16;                // keys of a slice
 constexpr int kWarps = 8;                 // workers of a CTA, one CTA an SM
 constexpr int kFewThreads = 32 * kWarps;
-constexpr int kMinRange = 4;
+constexpr int kMinRange = 6;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D, int MT> struct FC {
@@ -51,6 +51,7 @@ template <int D, int MT> struct FC {
 
 template <int MT> struct FewAux {
   int64_t pre[kFewThreads + 1];          // slices before each thread's sequences
+  TreeSeq seq[kFewThreads];              // the sequences, where a thread has one at most
   uint64_t full[kWarps][6];              // ring slots (DEPTH <= 6)
   uint4 anc[kWarps][16 * MT];            // what each row's token sees of its tree
   signed char par[kWarps][128];
@@ -100,12 +101,13 @@ struct Cursor {
   int64_t left;
   __device__ __forceinline__ void size() { nt = seq_slices(s); }
   // To slice 0 of the next item that has any (only while left > 0).
-  __device__ __forceinline__ void next_item(const TreeArgs& a) {
+  template <typename Seq>
+  __device__ __forceinline__ void next_item(int H, Seq seq) {
     j = 0;
-    if (++g < a.H) return;
+    if (++g < H) return;
     g = 0;
     do {
-      s = tree_seq(a, ++b);
+      s = seq(++b);
       size();
     } while (nt == 0);
   }
@@ -120,6 +122,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                 int part_rows, float* __restrict__ part_o, float2* __restrict__ part_ml,
                 TreeCut* __restrict__ cuts) {
   using C = FC<D, MT>;
+  pdl_trigger();  // the merge: its blocks come as this grid's leave
   pdl_wait();
   extern __shared__ __align__(1024) unsigned char dsm[];
   __shared__ FewAux<MT> aux;
@@ -144,6 +147,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     for (int b = min(a.B, tid * per); b < min(a.B, (tid + 1) * per); ++b) {
       const TreeSeq s = tree_seq(a, b);
       if (s.error && blockIdx.x == 0) record_error(a.status, s.error);
+      aux.seq[tid] = s;
       mine += (int64_t)seq_slices(s) * a.H;
     }
     int64_t incl = mine;
@@ -180,6 +184,12 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     return;
   }
 
+  // sequence b (shared memory: a read at an item's start is on the way of its
+  // loads)
+  auto seq = [&](int b) -> TreeSeq {
+    if (per == 1) return aux.seq[b];
+    return tree_seq(a, b);
+  };
   Cursor ld;  // the slice to load next
   {
     // the last thread whose sequences begin at or before slice lo
@@ -191,7 +201,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     int64_t at = aux.pre[t];
     ld.b = t * per;
     for (;;) {  // (its run holds lo, so this ends)
-      ld.s = tree_seq(a, ld.b);
+      ld.s = seq(ld.b);
       ld.size();
       const int64_t n = (int64_t)ld.nt * a.H;
       if (lo < at + n || ld.b + 1 >= a.B) break;
@@ -257,7 +267,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     }
     --ld.left;
     if (++ld.j == ld.nt && ld.left > 0) {
-      ld.next_item(a);
+      ld.next_item(a.H, seq);
       ids_fresh = true;
     }
   };
@@ -528,7 +538,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       }
     cu.left -= cnt;
     cu.j += cnt;
-    if (cu.left > 0) cu.next_item(a);
+    if (cu.left > 0) cu.next_item(a.H, seq);
   }
   if (!ok) {
     if (lane == 0) record_error(a.status, MSA_ERR_TIMEOUT);
@@ -541,7 +551,6 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       }
     }
   }
-  pdl_trigger();
 }
 
 struct FewPlan {
@@ -582,7 +591,7 @@ int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kFewThreads), C::SMEM, s, km, vm, kp, vp, a,
                           p.part_rows, part_o, part_ml, cuts))
     return rc;
-  return tree_merge_launch(a, D, (int)grid * kWarps, p.part_rows, part_o, part_ml, cuts, s);
+  return tree_merge_launch(a, D, (int)grid, kWarps, p.part_rows, part_o, part_ml, cuts, s);
 }
 
 }  // namespace

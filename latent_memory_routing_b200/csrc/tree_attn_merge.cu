@@ -4,83 +4,112 @@
 //   O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i,
 // in a fixed order.  It reads each partial once and is bound by the latency of
 // those loads (a few hundred KB in all), so many are in flight at a time: a
-// block takes up to 16 of an item's rows, and where there are fewer (a decode
-// step, whose items may have a hundred short parts) several warps share a
-// row's parts.  Blocks of workers that cut no item end at once.
+// block takes up to 16 of the cut rows that one CTA of the attention left, and
+// where there are fewer (one sequence's decode step, whose items have dozens
+// of short parts) several warps share a row's parts.
 #include "tree_attn.cuh"
 
 namespace msa {
 namespace {
 
 constexpr int kMergeWarps = 16;  // and rows of a block at most
-constexpr int kBatch = 8;  // parts a warp has in flight
+constexpr int kBatch = 8;       // partial rows a warp has in flight
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// blockIdx.x: the worker whose range start cuts the item; blockIdx.y: rows
-// kMergeWarps y .. of it.
+// Of workers [per x, per x + per), x = blockIdx.x, the rows that a border at
+// their range starts cuts: kMergeWarps of them, from kMergeWarps blockIdx.y on.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-tree_merge_kernel(const __grid_constant__ TreeArgs a, int part_rows,
+tree_merge_kernel(const __grid_constant__ TreeArgs a, int per, int part_rows,
                   const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                   const TreeCut* __restrict__ cuts) {
   constexpr int VEC = D / 32;
-  __shared__ float so[kMergeWarps][D];
+  __shared__ __align__(16) float so[kMergeWarps][D];
   __shared__ float2 sml[kMergeWarps];
   pdl_trigger();
   pdl_wait();
-  const TreeCut cut = cuts[blockIdx.x];
-  const int rows = cut.rows - (int)blockIdx.y * kMergeWarps;  // of this block
-  if (cut.last < 0 || rows <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int rp = 1;  // the rows, rounded up to a power of two
-  while (rp < min(rows, kMergeWarps)) rp <<= 1;
+  TreeCut cut{0, 0, 0, 0, -1};  // a lane a worker
+  if (lane < per) cut = cuts[blockIdx.x * per + lane];
+  int end = cut.last < 0 ? 0 : cut.rows;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, end, s);
+    if (lane >= s) end += v;
+  }
+  const int left = __shfl_sync(0xffffffffu, end, 31) - (int)blockIdx.y * kMergeWarps;
+  if (left <= 0) return;
+  int rp = 1;  // the block's rows, rounded up to a power of two
+  while (rp < min(left, kMergeWarps)) rp <<= 1;
   const int step = kMergeWarps / rp, sub = warp / rp;  // warps of a row, this one's turn
-  const int rr = blockIdx.y * kMergeWarps + warp % rp;
-  const bool live = rr < cut.rows;
-  const int n_parts = live ? cut.last - (int)blockIdx.x + 2 : 0;
+  const bool live = warp % rp < left;
+  const int at = blockIdx.y * kMergeWarps + warp % rp;
+  const int src = live ? __popc(__ballot_sync(0xffffffffu, end <= at)) : 0;  // its worker
+  cut.last = __shfl_sync(0xffffffffu, cut.last, src);
+  cut.t0 = __shfl_sync(0xffffffffu, cut.t0, src);
+  cut.g = __shfl_sync(0xffffffffu, cut.g, src);
+  cut.row0 = __shfl_sync(0xffffffffu, cut.row0, src);
+  cut.rows = __shfl_sync(0xffffffffu, cut.rows, src);
+  const int rr = at - (__shfl_sync(0xffffffffu, end, src) - cut.rows);
+  const int worker = blockIdx.x * per + src;
+  const int n_parts = live ? cut.last - worker + 2 : 0;
+  const int mine = (n_parts - sub + step - 1) / step;  // parts sub, sub + step, ..
+  // part 0 is (worker - 1, slot 1), part i (worker + i - 1, slot 0)
+  auto prow = [&](int i) {
+    const int p = sub + i * step;
+    return ((int64_t)(worker - 1 + p) * 2 + (p == 0 ? 1 : 0)) * part_rows + rr;
+  };
   float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
   for (int x = 0; x < VEC; ++x) o[x] = 0.f;
-  auto prow = [&](int i) {
-    const int64_t w = (int64_t)blockIdx.x - 1 + i;
-    return (w * 2 + (i == 0 ? 1 : 0)) * part_rows + rr;
-  };
-  auto join = [&](float2 ml, const float* v) {
-    if (ml.y == 0.f) return;  // no weight (a NaN sum joins)
-    const float mn = fmaxf(m, ml.x);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float c0 = exp2f(m - ref), c1 = ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref);
-    l = (l == 0.f ? 0.f : l * c0) + ml.y * c1;
-#pragma unroll
-    for (int x = 0; x < VEC; ++x) o[x] = o[x] * c0 + v[x] * c1;
-    m = mn;
-  };
-  for (int i = sub; i < n_parts; i += kBatch * step) {
-    float2 ml[kBatch];
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    // a lane a part: the weights 2^(m_i - m) of up to 32 parts
+    const int n = min(32, mine - i0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = part_ml[prow(i0 + lane)];
     float v[kBatch][VEC];
+    auto load = [&](int i) {
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const int p = i + x * step;
-      ml[x] = make_float2(-INFINITY, 0.f);
-      if (p < n_parts) {
-        const int64_t pr = prow(p);
-        ml[x] = part_ml[pr];
-        const float* src = part_o + pr * D + lane * VEC;
+      for (int b = 0; b < kBatch; ++b) {
+        const float* src = part_o + prow(i0 + min(i + b, n - 1)) * D + lane * VEC;
         if constexpr (VEC == 4) {
           const float4 f = *reinterpret_cast<const float4*>(src);
-          v[x][0] = f.x, v[x][1] = f.y, v[x][2] = f.z, v[x][3] = f.w;
+          v[b][0] = f.x, v[b][1] = f.y, v[b][2] = f.z, v[b][3] = f.w;
         } else {
           const float2 f = *reinterpret_cast<const float2*>(src);
-          v[x][0] = f.x, v[x][1] = f.y;
+          v[b][0] = f.x, v[b][1] = f.y;
         }
       }
-    }
+    };
+    load(0);  // in flight with the sums
+    float mx = ml.y == 0.f ? -INFINITY : ml.x;  // no weight (a NaN sum has one)
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) join(ml[x], v[x]);
+    for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+    const float c = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - ref);
+    const float w = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref);
+    float ls = ml.y == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+    l = (l == 0.f ? 0.f : l * c) + ls;
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) o[x] *= c;
+    m = mn;
+    for (int i = 0;;) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float wb = __shfl_sync(0xffffffffu, w, min(i + b, 31));
+#pragma unroll
+        for (int x = 0; x < VEC; ++x)
+          if (i + b < n && wb != 0.f) o[x] = fmaf(v[b][x], wb, o[x]);
+      }
+      if ((i += kBatch) >= n) break;
+      load(i);
+    }
   }
   if (step > 1) {
     if (lane == 0) sml[warp] = make_float2(m, l);
@@ -89,8 +118,18 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int part_rows,
     __syncthreads();
     if (sub > 0) return;
 #pragma unroll 1
-    for (int i = 1; i < min(n_parts, step); ++i)
-      join(sml[warp + i * rp], &so[warp + i * rp][lane * VEC]);
+    for (int i = 1; i < min(n_parts, step); ++i) {
+      const float2 ml = sml[warp + i * rp];
+      if (ml.y == 0.f) continue;
+      const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+      const float c = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - ref);
+      const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - ref);
+      l = (l == 0.f ? 0.f : l * c) + w * ml.y;
+#pragma unroll
+      for (int x = 0; x < VEC; ++x)
+        o[x] = fmaf(so[warp + i * rp][lane * VEC + x], w, o[x] * c);
+      m = mn;
+    }
   }
   if (!live) return;
   const int row = cut.row0 + rr;
@@ -103,19 +142,20 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int part_rows,
 }
 
 template <int D>
-int launch(const TreeArgs& a, int workers, int part_rows, const float* part_o,
+int launch(const TreeArgs& a, int ctas, int per, int part_rows, const float* part_o,
            const float2* part_ml, const TreeCut* cuts, cudaStream_t s) {
   return launch_pdl(tree_merge_kernel<D>,
-                    dim3(workers, (part_rows + kMergeWarps - 1) / kMergeWarps),
-                    dim3(32 * kMergeWarps), 0, s, a, part_rows, part_o, part_ml, cuts);
+                    dim3(ctas, (per * part_rows + kMergeWarps - 1) / kMergeWarps),
+                    dim3(32 * kMergeWarps), 0, s, a, per, part_rows, part_o, part_ml, cuts);
 }
 
 }  // namespace
 
-int tree_merge_launch(const TreeArgs& a, int D, int workers, int part_rows, const float* part_o,
-                      const float2* part_ml, const TreeCut* cuts, cudaStream_t s) {
-  return D == 64 ? launch<64>(a, workers, part_rows, part_o, part_ml, cuts, s)
-                 : launch<128>(a, workers, part_rows, part_o, part_ml, cuts, s);
+int tree_merge_launch(const TreeArgs& a, int D, int ctas, int per, int part_rows,
+                      const float* part_o, const float2* part_ml, const TreeCut* cuts,
+                      cudaStream_t s) {
+  return D == 64 ? launch<64>(a, ctas, per, part_rows, part_o, part_ml, cuts, s)
+                 : launch<128>(a, ctas, per, part_rows, part_o, part_ml, cuts, s);
 }
 
 }  // namespace msa
