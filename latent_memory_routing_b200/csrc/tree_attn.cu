@@ -255,7 +255,8 @@ int tree_body(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int 
               size_t ws_bytes, cudaStream_t s) {
   if (int rc = tree_shape(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size)) return rc;
   if (n_tok < 0 || n_pages <= 0 || !std::isfinite(scale)) return MSA_ERR_INVALID_ARG;
-  if ((int64_t)n_pages * H * page_size > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  if ((int64_t)n_pages * H * page_size > INT32_MAX || n_tok > INT32_MAX)
+    return MSA_ERR_UNSUPPORTED;
   if (!tok_offsets || !block_table || !cache_len || !k_pages || !v_pages)
     return MSA_ERR_INVALID_ARG;
   if (m_cap > 0 && (!k_mem || !v_mem || !mem_len)) return MSA_ERR_INVALID_ARG;

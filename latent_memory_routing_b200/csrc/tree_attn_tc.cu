@@ -14,7 +14,10 @@
 //
 // Design.
 //   * Even work: the 128-key tiles of all (sequence, KV head, row block)
-//     items in one line, cut into one contiguous range a CTA (one CTA an SM).
+//     items in one line, each item's behind kItemCost units that stand for its
+//     start and end (about 12,000 cycles, 3 tiles' time: without them a CTA of
+//     short items ended at 248,000 cycles, the others at 145,000), cut into
+//     one contiguous range a CTA (one CTA an SM).
 //     An item inside one range is written directly; an item cut by a range
 //     border is written as fp32 partials (at most two a CTA) that a second
 //     launch merges in a fixed order.  The lengths stay on the device: every
@@ -52,6 +55,7 @@ constexpr int kTcThreads = 384; // 4 single warps, 2 softmax warpgroups
 constexpr int kMaxSt = 6;       // K or V ring slots at most
 constexpr int kSched = 3;       // published items
 constexpr int kReaders = 11;    // K warp, V warp, MMA, 8 softmax warps
+constexpr int kItemCost = 3;    // what an item's start and end cost, in tiles
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -77,12 +81,13 @@ struct ItemE {
 struct Aux {
   uint64_t kfull[kMaxSt], kfree[kMaxSt], vfull[kMaxSt], vfree[kMaxSt];
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_empty[2], ml_full;
-  uint64_t sched_full[kSched], sched_empty[kSched];
+  uint64_t sched_full[kSched], par_full[kSched], sched_empty[kSched];
   ItemE item[kSched];
   int bad[kSched];             // item ordinal + 1 where V held non-finite drafted values
   float2 ml[128];              // (m, l) of the stream that does not finish the item
   signed char par[kSched][128];  // the published items' parents: -1 root, -2 pruned
   int64_t start;               // first tile of the range within its sequence
+  TreeSeq start_seq;
   int start_b;
   uint32_t tmem_base;
   int abort_flag;
@@ -134,14 +139,16 @@ __device__ __forceinline__ int seq_tiles(const TreeSeq& s) {
 
 template <int D, int kQT>
 __global__ void __launch_bounds__(kTcThreads, 1)
-tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant__ CUtensorMap tm_vm,
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+               const __grid_constant__ CUtensorMap tm_km, const __grid_constant__ CUtensorMap tm_vm,
                const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
-               const __grid_constant__ TreeArgs a, int part_rows, int q_rows, int n_k,
-               int n_v, float* __restrict__ part_o, float2* __restrict__ part_ml,
+               const __grid_constant__ TreeArgs a, int part_rows, int tile_rows,
+               int q_rows, int n_k, int n_v, float* __restrict__ part_o, float2* __restrict__ part_ml,
                TreeCut* __restrict__ cuts) {
   using C = TC<D>;
   constexpr int KB = C::KB;
-  constexpr int kBlkRows = 128 * kQT;
+  const int blk_rows = tile_rows * kQT;  // rows of an item: whole tokens
+  pdl_trigger();  // the merge: its blocks come as this grid's leave
   pdl_wait();
   extern __shared__ __align__(1024) unsigned char dsm[];
   unsigned char* base = tc::smem_align<1024>(dsm);
@@ -172,11 +179,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
     tc::mbar_init(&aux.ml_full, 4);
     for (int i = 0; i < kSched; ++i) {
       tc::mbar_init(&aux.sched_full[i], 1);
+      tc::mbar_init(&aux.par_full[i], 1);
       tc::mbar_init(&aux.sched_empty[i], kReaders);
       aux.bad[i] = 0;
     }
     aux.abort_flag = 0;
     tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&tm_kp);
+    tc::tma_prefetch_desc(&tm_vp);
+    tc::tma_prefetch_desc(&tm_km);
+    tc::tma_prefetch_desc(&tm_vm);
   }
   if (warp == 1) {
     tc::tmem_alloc(&aux.tmem_base, 512);
@@ -186,8 +198,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
   // This CTA's range: thread t sums the tiles of its run of sequences, a scan
   // over the threads places them, and the thread that holds the range's first
   // tile finds its sequence.
-  auto tiles_of = [&](const TreeSeq& s) -> int64_t {
-    return (int64_t)seq_tiles(s) * ((s.n * G + kBlkRows - 1) / kBlkRows) * a.H;
+  auto units_of = [&](const TreeSeq& s) -> int64_t {
+    const int nt = seq_tiles(s);
+    if (nt == 0) return 0;
+    return (int64_t)(nt + kItemCost) * ((s.n * G + blk_rows - 1) / blk_rows) * a.H;
   };
   int64_t* wsum = reinterpret_cast<int64_t*>(sK);  // [12], before any tile lands there
   const int per = (a.B + kTcThreads - 1) / kTcThreads;
@@ -196,7 +210,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
   for (int b = b_lo; b < b_hi; ++b) {
     const TreeSeq s = tree_seq(a, b);
     if (s.error && blockIdx.x == 0) record_error(a.status, s.error);
-    mine += tiles_of(s);
+    mine += units_of(s);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -219,9 +233,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
   int64_t at = before + incl - mine;
   if (lo < hi && lo >= at && lo < at + mine) {
     for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t t = tiles_of(tree_seq(a, b));
+      const TreeSeq s = tree_seq(a, b);
+      const int64_t t = units_of(s);
       if (lo < at + t) {
         aux.start_b = b;
+        aux.start_seq = s;
         aux.start = lo - at;
         break;
       }
@@ -251,62 +267,74 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
     if (warp == 2) {
       // --------------------------------------------- the range and the queries
       int64_t left = hi - lo;
-      int b = 0, item = 0, j = 0;
+      int b = 0, item = 0;
       TreeSeq s{};
       int nt = 0, nblk = 0;
-      auto load_seq = [&]() {
-        s = tree_seq(a, b);
+      auto size_seq = [&]() {
         nt = seq_tiles(s);
-        nblk = (s.n * G + kBlkRows - 1) / kBlkRows;
+        nblk = (s.n * G + blk_rows - 1) / blk_rows;
       };
       TreeCut cut{0, 0, 0, 0, -1};
+      int pos = 0;  // units of the item at hand that lie before the range
       if (left > 0) {
         b = aux.start_b;
-        load_seq();
-        item = (int)(aux.start / nt);
-        j = (int)(aux.start % nt);
-        if (j > 0 && range_lo(blockIdx.x - 1) <= lo - j) {
-          // the first border inside this item: its last part holds tile `end`
-          const int64_t end = lo - j + nt - 1;
+        s = aux.start_seq;
+        size_seq();
+        item = (int)(aux.start / (nt + kItemCost));
+        pos = (int)(aux.start % (nt + kItemCost));
+        if (pos > kItemCost && range_lo(blockIdx.x - 1) <= lo - pos + kItemCost) {
+          // the first border inside this item's tiles: its last part holds the
+          // item's last unit, `end`
+          const int64_t end = lo - pos + kItemCost + nt - 1;
           int64_t c = min(ge - 1, end * ge / total);
           while (c + 1 < ge && range_lo(c + 1) <= end) ++c;
           while (range_lo(c) > end) --c;
           cut.last = (int)c;
           cut.t0 = s.t0;
           cut.g = item / nblk;
-          cut.row0 = item % nblk * kBlkRows;
-          cut.rows = min(kBlkRows, s.n * G - cut.row0);
+          cut.row0 = item % nblk * blk_rows;
+          cut.rows = min(blk_rows, s.n * G - cut.row0);
         }
       }
       if (lane == 0) cuts[blockIdx.x] = cut;
+      uint32_t q_loads = 0;
       for (uint32_t k = 0;; ++k) {
         const int slot = k % kSched;
         if (!wait(&aux.sched_empty[slot], ((k / kSched) & 1) ^ 1)) break;
         ItemE e{};
         e.cnt = -1;
-        if (left > 0) {
+        while (left > 0) {
           while (item == a.H * nblk || nt == 0) {  // the next sequence with tiles
-            ++b;
-            load_seq();
+            s = tree_seq(a, ++b);
+            size_seq();
             item = 0;
           }
+          const int take = (int)min((int64_t)(nt + kItemCost - pos), left);
+          const int j_lo = max(pos - kItemCost, 0), j_hi = max(pos + take - kItemCost, 0);
+          const int at = item++;
+          left -= take;
+          pos = 0;
+          if (j_lo == j_hi) continue;  // the border lies before its first tile
           e.t0 = s.t0;
           e.n = s.n;
           e.M = s.M;
           e.L = s.L;
           e.cache = s.cache;
           e.b = b;
-          e.g = item / nblk;
-          e.row0 = item % nblk * kBlkRows;
-          e.rows = min(kBlkRows, s.n * G - e.row0);
-          e.j_lo = j;
-          e.cnt = (int)min((int64_t)(nt - j), left);
-          e.part = j > 0 ? 0 : e.cnt < nt ? 1 : -1;
-          left -= e.cnt;
-          ++item;
-          j = 0;
+          e.g = at / nblk;
+          e.row0 = at % nblk * blk_rows;
+          e.rows = min(blk_rows, s.n * G - e.row0);
+          e.j_lo = j_lo;
+          e.cnt = j_hi - j_lo;
+          e.part = j_lo > 0 ? 0 : j_hi < nt ? 1 : -1;
+          break;
         }
-        if (a.parents && e.cnt > 0) {
+        if (lane == 0) {
+          aux.item[slot] = e;
+          tc::mbar_arrive(&aux.sched_full[slot]);
+        }
+        if (e.cnt < 0) break;
+        if (a.parents) {
           for (int i = lane; i < e.n; i += 32) {
             int p = a.parents[e.t0 + i];
             if (p >= i) {  // a parent comes before its child
@@ -316,34 +344,30 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
             aux.par[slot][i] = (signed char)max(p, -2);
           }
           __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&aux.par_full[slot]);
         }
-        if (lane == 0) {
-          aux.item[slot] = e;
-          tc::mbar_arrive(&aux.sched_full[slot]);
-        }
-        if (e.cnt < 0) break;
-        // its query rows, into buffer k & 1 (kQT = 1) or the two tiles
+        // its query rows, into buffer k & 1 (kQT = 1) or the two tiles (rows of
+        // tokens behind the sequence's come along: nobody reads their S)
         const int qb = kQT == 1 ? k & 1 : 0;
         const uint32_t use = kQT == 1 ? k >> 1 : k;
         if (use > 0 && !wait(&aux.q_free[qb], (use - 1) & 1)) break;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-        for (int c = lane; c < e.rows * (D / 8); c += 32) {
-          const int r = c / (D / 8), ch = c % (D / 8);
-          const int row = e.row0 + r;
-          const __nv_bfloat16* src =
-              q + ((e.t0 + row / G) * a.Hq + e.g * G + row % G) * D + ch * 8;
-          const int tile = kQT == 1 ? qb : r >> 7, rr = kQT == 1 ? r : r & 127;
-          unsigned char* dst = sQ + tile * q_tile + (ch >> 3) * (q_rows * 128) + rr * 128 +
-                               (((ch & 7) ^ (rr & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)),
-                       "l"(src)
-                       : "memory");
+        if (lane == 0) {
+          const int tiles = kQT == 1 ? 1 : 2;
+          tc::mbar_arrive_expect_tx(&aux.q_full[qb], (uint32_t)(tiles * KB * tile_rows * 128));
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              tc::tma_load_3d(sQ + (kQT == 1 ? qb : t) * q_tile + kb * (q_rows * 128), &tm_q,
+                              &aux.q_full[qb], kb * 64, e.g * G,
+                              (int)(e.t0 + (e.row0 + t * tile_rows) / G));
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        tc::fence_proxy_async_smem();
+        ++q_loads;
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&aux.q_full[qb]);
       }
+      // the last loads of both buffers land before the CTA exits
+      constexpr uint32_t kBufs = kQT == 1 ? 2 : 1;
+      for (uint32_t v = q_loads > kBufs ? q_loads - kBufs : 0; v < q_loads; ++v)
+        tc::mbar_wait(&aux.q_full[v % kBufs], (v / kBufs) & 1);
     } else if (warp == 0 || warp == 3) {
       // ----------------------------------------------------------- K, V loads
       const bool isv = warp == 3;
@@ -417,95 +441,145 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
       // v >> 1 (kQT = 2) of the range.  S(v) may follow once P V(v - 2),
       // which reads the same TMEM columns, has been issued (one thread's
       // MMAs run in issue order), so S(v)'s commit also says that P V(v - 2)
-      // is done.  P V and S are issued as they become ready.
-      struct Walk {
-        uint32_t k;     // items taken
-        int i, cnt;     // key tile within the item's share
+      // is done.
+      auto issue_s = [&](int s, int q_at, int st) {
+        tc::tc_fence_after();
+        const uint64_t qd = tc::sdesc_kmajor_sw128(tc::smem_u32(sQ + q_at * q_tile));
+        const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(sK + st * C::TILE));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_bf16_ss(tmem + s * 128,
+                          tc::desc_add(qd, (kk >> 2) * (q_rows * 128) + (kk & 3) * 32),
+                          tc::desc_add(kd, (kk >> 2) * (kKeys * 128) + (kk & 3) * 32),
+                          C::IDESC_S, kk > 0 ? 1u : 0u);
+        tc::mma_commit(&aux.s_full[s]);
       };
-      Walk ws{0, 0, 0}, wp{0, 0, 0};
+      auto issue_pv = [&](int s, int st, uint32_t acc) {
+        tc::tc_fence_after();
+        const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(sV + st * C::TILE), kKeys * 128);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc::mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8,
+                          tc::desc_add(vd, kk * 16 * 128), C::IDESC_O, kk > 0 ? 1u : acc);
+      };
+     if constexpr (kQT == 2) {
+      // Both streams on every tile, in a fixed order: P V_0 S_0 P V_1 S_1 of
+      // consecutive tiles (what this thread does between two MMAs is time that
+      // the tensor pipe idles: as one loop that polls for whichever is ready a
+      // tile took 4,000 cycles, this UNMEASURED); at an item's end both P V
+      // first, since the next item's queries are still on their way.
+      uint32_t tiles = 0;         // key tiles whose P V are issued
+      int kst = 0, vst = 0;
+      uint32_t kph = 0, vph = 0;
+      auto next_k = [&]() {
+        tc::mma_commit(&aux.kfree[kst]);
+        if (++kst == n_k) {
+          kst = 0;
+          kph ^= 1;
+        }
+      };
+      for (uint32_t k = 0;; ++k) {
+        const int slot = k % kSched;
+        if (!wait(&aux.sched_full[slot], (k / kSched) & 1)) break;
+        const int cnt = aux.item[slot].cnt;
+        tc::mbar_arrive(&aux.sched_empty[slot]);
+        if (cnt < 0) break;
+        if (!wait(&aux.q_full[0], k & 1) || !wait(&aux.kfull[kst], kph)) break;
+        issue_s(0, 0, kst);
+        issue_s(1, 1, kst);
+        next_k();
+        if (cnt == 1) tc::mma_commit(&aux.q_free[0]);
+        bool ok = true;
+        for (int j = 0; ok && j < cnt; ++j, ++tiles) {
+          const bool more = j + 1 < cnt;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (s == 0) ok = ok && wait(&aux.vfull[vst], vph);
+            if (j == 0 && k > 0) ok = ok && wait(&aux.o_empty[s], (k - 1) & 1);
+            ok = ok && wait(&aux.p_full[s], tiles & 1);
+            if (!ok) break;
+            issue_pv(s, vst, j > 0 ? 1u : 0u);
+            if (!more) {
+              tc::mma_commit(&aux.o_full[s]);
+            } else {
+              if (s == 0 && !(ok = wait(&aux.kfull[kst], kph))) break;
+              issue_s(s, s, kst);
+            }
+          }
+          if (!ok) break;
+          if (more) {
+            next_k();
+            if (j + 2 == cnt) tc::mma_commit(&aux.q_free[0]);
+          }
+          tc::mma_commit(&aux.vfree[vst]);
+          if (++vst == n_v) {
+            vst = 0;
+            vph ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+     } else {
+      // One key tile a stream in turn; P V and S are issued as they become
+      // ready (the loads set the pace, and neither waits for the other's).
+      uint32_t ks = 0, kp = 0;   // items taken by S, by P V
+      int i_s = 0, n_s = 0;      // key tile within the item's share, tiles of it
+      int i_p = 0, n_p = 0;
       uint32_t vs = 0, vp = 0;   // S and P V issued
       uint32_t ne[2] = {0, 0};   // items whose O a stream has begun
       int kst = 0, vst = 0;      // ring slots of the next S and P V
       uint32_t kph = 0, vph = 0;
-      bool have = false, done = false;
-      uint64_t t_last = tc::globaltimer_ns();
+      bool done = false, q_seen = false;
+      uint64_t t_last = 0;
       uint32_t polls = 0;
       while (!(done && vp == vs)) {
         bool moved = false;
-        if (vp < vs) {
+        if (vp < vs && tc::mbar_test(&aux.p_full[vp & 1], (vp >> 1) & 1)) {
           const int s = vp & 1;
-          if (tc::mbar_test(&aux.p_full[s], (vp >> 1) & 1)) {
-            if (wp.i == wp.cnt) {  // published: S has read it
-              const int slot = wp.k % kSched;
-              wp.cnt = aux.item[slot].cnt;
-              wp.i = 0;
-              ++wp.k;
-              tc::mbar_arrive(&aux.sched_empty[slot]);
-            }
-            const bool first = kQT == 1 ? wp.i < 2 : wp.i == 0;
-            const bool last = kQT == 1 ? wp.i + 2 >= wp.cnt : wp.i + 1 == wp.cnt;
-            if ((!first || ne[s] == 0 || tc::mbar_test(&aux.o_empty[s], (ne[s] - 1) & 1)) &&
-                tc::mbar_test(&aux.vfull[vst], vph)) {
-              if (first) ++ne[s];
-              tc::tc_fence_after();
-              const uint64_t vd =
-                  tc::sdesc_mnmajor_sw128(tc::smem_u32(sV + vst * C::TILE), kKeys * 128);
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc::mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8,
-                                tc::desc_add(vd, kk * 16 * 128), C::IDESC_O,
-                                (!first || kk > 0) ? 1u : 0u);
-              if (last) tc::mma_commit(&aux.o_full[s]);
-              if (kQT == 1 || s == 1) {
-                tc::mma_commit(&aux.vfree[vst]);
-                if (++vst == n_v) {
-                  vst = 0;
-                  vph ^= 1;
-                }
-                ++wp.i;
-              }
-              ++vp;
-              moved = true;
-            }
+          if (i_p == n_p) {  // published: S has read it
+            const int slot = kp % kSched;
+            n_p = aux.item[slot].cnt;
+            i_p = 0;
+            ++kp;
+            tc::mbar_arrive(&aux.sched_empty[slot]);
           }
-        }
-        if (!done && vs < vp + 2) {
-          if (!have && tc::mbar_test(&aux.sched_full[ws.k % kSched], (ws.k / kSched) & 1)) {
-            ws.cnt = aux.item[ws.k % kSched].cnt;
-            ws.i = 0;
-            have = ws.cnt > 0;
-            done = !have;
-            ++ws.k;
+          const bool first = i_p < 2;
+          if ((!first || ne[s] == 0 || tc::mbar_test(&aux.o_empty[s], (ne[s] - 1) & 1)) &&
+              tc::mbar_test(&aux.vfull[vst], vph)) {
+            if (first) ++ne[s];
+            issue_pv(s, vst, first ? 0u : 1u);
+            if (i_p + 2 >= n_p) tc::mma_commit(&aux.o_full[s]);
+            tc::mma_commit(&aux.vfree[vst]);
+            if (++vst == n_v) {
+              vst = 0;
+              vph ^= 1;
+            }
+            ++i_p;
+            ++vp;
             moved = true;
           }
-          if (have) {
-            const uint32_t ord = ws.k - 1;
-            const int qb = kQT == 1 ? ord & 1 : 0;
-            const uint32_t use = kQT == 1 ? ord >> 1 : ord;
-            if (tc::mbar_test(&aux.q_full[qb], use & 1) && tc::mbar_test(&aux.kfull[kst], kph)) {
-              const int s = vs & 1;
-              tc::tc_fence_after();
-              const uint64_t qd = tc::sdesc_kmajor_sw128(
-                  tc::smem_u32(sQ + (kQT == 1 ? qb : s) * q_tile));
-              const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(sK + kst * C::TILE));
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_bf16_ss(tmem + s * 128,
-                                tc::desc_add(qd, (kk >> 2) * (q_rows * 128) + (kk & 3) * 32),
-                                tc::desc_add(kd, (kk >> 2) * (kKeys * 128) + (kk & 3) * 32),
-                                C::IDESC_S, kk > 0 ? 1u : 0u);
-              tc::mma_commit(&aux.s_full[s]);
-              if (kQT == 1 || s == 1) {
-                tc::mma_commit(&aux.kfree[kst]);
-                if (++kst == n_k) {
-                  kst = 0;
-                  kph ^= 1;
-                }
-                if (++ws.i == ws.cnt) {
-                  tc::mma_commit(&aux.q_free[qb]);
-                  have = false;
-                }
+        }
+        if (vs < vp + 2 && !done) {
+          if (i_s == n_s && tc::mbar_test(&aux.sched_full[ks % kSched], (ks / kSched) & 1)) {
+            n_s = aux.item[ks % kSched].cnt;
+            i_s = 0;
+            done = n_s < 0;
+            if (done) n_s = 0;
+            ++ks;
+            q_seen = false;
+          }
+          if (i_s < n_s) {
+            const int s = vs & 1;
+            const int qb = (ks - 1) & 1;
+            if (!q_seen) q_seen = tc::mbar_test(&aux.q_full[qb], ((ks - 1) >> 1) & 1);
+            if (q_seen && tc::mbar_test(&aux.kfull[kst], kph)) {
+              issue_s(s, qb, kst);
+              tc::mma_commit(&aux.kfree[kst]);
+              if (++kst == n_k) {
+                kst = 0;
+                kph ^= 1;
               }
+              if (++i_s == n_s) tc::mma_commit(&aux.q_free[qb]);
               ++vs;
               moved = true;
             }
@@ -524,6 +598,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
           }
         }
       }
+     }
     }
   } else {
     // --------------------------------------------------------------- softmax
@@ -547,9 +622,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
       const int step = kQT == 1 ? 2 : 1;
       const bool both = kQT == 1 && e.cnt >= 2;     // both streams hold a part of O
       const int owner = kQT == 1 ? (u + e.cnt - 1) & 1 : grp;
-      const int rb = (kQT == 2 ? grp * 128 : 0) + r;  // row within the block
-      const bool row_ok = rb < e.rows;
-      const bool warp_on = (kQT == 2 ? grp * 128 : 0) + quad * 32 < e.rows;
+      const int rb = (kQT == 2 ? grp * tile_rows : 0) + r;  // row within the block
+      const bool row_ok = r < tile_rows && rb < e.rows;
+      const bool warp_on = (kQT == 2 ? grp * tile_rows : 0) + quad * 32 < e.rows;
       const int row = e.row0 + rb;
       const int tok = row / G;
       u128 anc = 0;
@@ -557,14 +632,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
         // what the row's token sees of its tree
         if (!a.parents) {
           anc = low_bits(tok + 1);
-        } else if (row_ok) {
-          const signed char* par = aux.par[slot];
-          int x = tok;
-          do {
-            anc |= (u128)1 << x;
-            x = par[x];
-          } while (x >= 0);
-          if (x != -1) anc = 0;  // pruned: sees nothing
+        } else {
+          if (!wait(&aux.par_full[slot], (k / kSched) & 1)) break;
+          if (row_ok) {
+            const signed char* par = aux.par[slot];
+            int x = tok;
+            do {
+              anc |= (u128)1 << x;
+              x = par[x];
+            } while (x >= 0);
+            if (x != -1) anc = 0;  // pruned: sees nothing
+          }
         }
       }
       __syncwarp();
@@ -588,27 +666,23 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
             const uint32_t vi = u + i;
             if (!wait(&aux.vfull[vi % n_v], (vi / n_v) & 1)) break;
             unsigned char* vr = sV + (vi % n_v) * C::TILE + r * 128;
-            if (r >= n_rows) {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-            } else if (!mem && key0 + r >= e.L) {
-              bool bad = false;
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) {
-                uint4* p =
-                    reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4));
+            bool bad = false;
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4));
+              if (r >= n_rows) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else if (!mem && key0 + r >= e.L) {
                 const uint4 x = *p;
-                const uint4 y =
-                    make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
+                const uint4 y = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y),
+                                           finite_bf16x2(x.z), finite_bf16x2(x.w));
                 if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
                   *p = y;
                   bad = true;
                 }
               }
-              if (bad) *(volatile int*)&aux.bad[k % kSched] = (int)k + 1;
             }
+            if (bad) *(volatile int*)&aux.bad[k % kSched] = (int)k + 1;
             tc::fence_proxy_async_smem();
           }
           if (warp_on) {
@@ -657,7 +731,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
             }
             if (t > 0 && __any_sync(0xffffffffu, grow && alpha != 0.f)) {
               const uint32_t tO = tmem + 256 + grp * D + lane_addr;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tc::tmem_ld32(tO + c * 32, o);
@@ -709,78 +783,84 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
           if (lane == 0) tc::mbar_arrive(&aux.ml_full);
         } else {
           if (!wait(&aux.o_full[grp], ne[grp] & 1)) break;
-          float c0 = 1.f, c1 = 0.f;
-          bool use0 = l_run != 0.f, use1 = false;
+          // O = c0 O_grp + c1 O_other; a part without weight is left out (its O
+          // may hold 0 times NaN): c = 0
+          float c0 = l_run == 0.f ? 0.f : 1.f, c1 = 0.f;
           if (both) {
             if (!wait(&aux.o_full[grp ^ 1], ne[grp ^ 1] & 1)) break;
             if (!wait(&aux.ml_full, n_pub & 1)) break;
             const float2 x = aux.ml[r];
             const float m = fmaxf(m_run, x.x);
-            c0 = m == -INFINITY ? 1.f : ex2a(m_run - m);
-            c1 = m == -INFINITY ? 1.f : ex2a(x.x - m);
-            use1 = x.y != 0.f;
-            l_run = (use0 ? c0 * l_run : 0.f) + (use1 ? c1 * x.y : 0.f);
+            c0 = l_run == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2a(m_run - m);
+            c1 = x.y == 0.f ? 0.f : m == -INFINITY ? 1.f : ex2a(x.x - m);
+            l_run = (l_run == 0.f ? 0.f : c0 * l_run) + (x.y == 0.f ? 0.f : c1 * x.y);
             m_run = m;
           }
           tc::tc_fence_after();
           const bool bad = *(volatile int*)&aux.bad[k % kSched] == (int)k + 1;
-          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-          const int64_t orow = (e.t0 + tok) * a.Hq + e.g * G + row % G;
+          if (e.part < 0) {
+            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            c0 *= inv;
+            c1 *= inv;
+          }
+          // (a small loop: this code runs once an item, and what it costs first
+          // is its way into the instruction cache)
           const int64_t prow = ((int64_t)blockIdx.x * 2 + e.part) * part_rows + rb;
           if (warp_on) {
             const uint32_t tO = tmem + 256 + grp * D + lane_addr;
-            const uint32_t tO2 = tmem + 256 + (grp ^ 1) * D + lane_addr;
-            // unrolled only as far as registers allow
+            const uint32_t tO2 = tmem + 256 + (both ? grp ^ 1 : grp) * D + lane_addr;
+            __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
+                                ((e.t0 + tok) * a.Hq + e.g * G + row % G) * D;
+            float* po = part_o + prow * D;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x0[32], x1[32];
-              float o[32];
-              tc::tmem_ld32(tO + c * 32, x0);
-              if (both) tc::tmem_ld32(tO2 + c * 32, x1);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t x0[16], x1[16];
+              float o[16];
+              tc::tmem_ld16(tO + c, x0);
+              tc::tmem_ld16(tO2 + c, x1);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) {
-                o[x] = use0 ? c0 * __uint_as_float(x0[x]) : 0.f;
-                if (both) o[x] += use1 ? c1 * __uint_as_float(x1[x]) : 0.f;
-              }
+              for (int x = 0; x < 16; ++x)
+                o[x] = (c0 == 0.f ? 0.f : c0 * __uint_as_float(x0[x])) +
+                       (c1 == 0.f ? 0.f : c1 * __uint_as_float(x1[x]));
               if (row_ok) {
-                if (bad) {
-                  // drafted values taken out of V, for the rows that see them
-                  for (int d = 0; d < e.n; ++d) {
-                    const int kr = e.L + d, j = n_mt + kr / kKeys;
-                    if (!((anc >> d) & 1) || j < e.j_lo || j >= e.j_lo + e.cnt || kr >= e.cache)
-                      continue;
-                    const int pg = a.block_table[(int64_t)e.b * a.max_pages + kr / a.page_size];
-                    if (pg < 0 || pg >= a.n_pages) continue;
-                    const __nv_bfloat16* v =
-                        static_cast<const __nv_bfloat16*>(a.v_pages) +
-                        (((int64_t)pg * a.H + e.g) * a.page_size + kr % a.page_size) * D + c * 32;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                      const float f = __bfloat162float(v[x]);
-                      if (!isfinite(f)) o[x] += f;
-                    }
-                  }
-                }
                 if (e.part < 0) {
-                  __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32;
 #pragma unroll
-                  for (int x = 0; x < 32; x += 8)
-                    st16(op + x, make_uint4(pack2(o[x] * inv, o[x + 1] * inv),
-                                            pack2(o[x + 2] * inv, o[x + 3] * inv),
-                                            pack2(o[x + 4] * inv, o[x + 5] * inv),
-                                            pack2(o[x + 6] * inv, o[x + 7] * inv)));
+                  for (int x = 0; x < 16; x += 8)
+                    st16(op + c + x,
+                         make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]),
+                                    pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7])));
                 } else {
-                  float* po = part_o + prow * D + c * 32;
 #pragma unroll
-                  for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<float4*>(po + x) =
+                  for (int x = 0; x < 16; x += 4)
+                    *reinterpret_cast<float4*>(po + c + x) =
                         make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                 }
               }
               __syncwarp();  // the next load is the whole warp's
             }
             if (row_ok && e.part >= 0) part_ml[prow] = make_float2(m_run, l_run);
+            if (row_ok && bad) {
+              // drafted values taken out of V, added for the rows that see them
+#pragma unroll 1
+              for (int d = 0; d < e.n; ++d) {
+                const int kr = e.L + d, j = n_mt + kr / kKeys;
+                if (!((anc >> d) & 1) || j < e.j_lo || j >= e.j_lo + e.cnt || kr >= e.cache)
+                  continue;
+                const int pg = a.block_table[(int64_t)e.b * a.max_pages + kr / a.page_size];
+                if (pg < 0 || pg >= a.n_pages) continue;
+                const __nv_bfloat16* v =
+                    static_cast<const __nv_bfloat16*>(a.v_pages) +
+                    (((int64_t)pg * a.H + e.g) * a.page_size + kr % a.page_size) * D;
+#pragma unroll 1
+                for (int x = 0; x < D; ++x) {
+                  const float f = __bfloat162float(v[x]);
+                  if (isfinite(f)) continue;
+                  if (e.part < 0) op[x] = __float2bfloat16(__bfloat162float(op[x]) + f);
+                  else po[x] += f;
+                }
+              }
+            }
           }
           tc::tc_fence_before();
           __syncwarp();
@@ -803,7 +883,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
     }
   }
 
-  pdl_trigger();
   tc::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -815,20 +894,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_km, const __grid_constant_
 struct TcPlan {
   int qt;          // Q tiles of an item
   int part_rows;   // rows of a partial
+  int tile_tok;    // tokens of a tile: whole tokens, at most 128 rows
   int q_rows, n_k, n_v;
   size_t smem, po_bytes, ml_bytes, cut_bytes, total;
 };
 
 // kQT = 2 once an item's rows exceed one MMA tile: both tiles then share one
-// pass over K and V.  The Q buffers hold no more rows than a sequence can
-// have (the MMA reads on into the ring: rows of S that nobody reads), what
+// pass over K and V.  The Q buffers hold no more rows than a tile can have
+// (the MMA reads on into the ring: rows of S that nobody reads), what
 // they leave goes to the rings.
 TcPlan tc_plan(int n_max, int G, int D) {
   TcPlan p{};
   const int rows = n_max * G;
   p.qt = rows > 128 ? 2 : 1;
-  p.part_rows = std::min(rows, 128 * p.qt);
-  p.q_rows = p.qt == 2 ? 128 : (rows + 7) / 8 * 8;
+  p.tile_tok = std::min(n_max, 128 / G);
+  p.part_rows = std::min(rows, p.tile_tok * G * p.qt);
+  p.q_rows = (p.tile_tok * G + 7) / 8 * 8;
   const int tile = D / 64 * kKeys * 128;
   const int q_bytes = 2 * (D / 64) * p.q_rows * 128;
   const int slots = (kSmemMax - 1024 - (int)sizeof(Aux) - q_bytes) / tile;
@@ -849,9 +930,10 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   float* part_o = reinterpret_cast<float*>(w);
   float2* part_ml = reinterpret_cast<float2*>(w + p.po_bytes);
   TreeCut* cuts = reinterpret_cast<TreeCut*>(w + p.po_bytes + p.ml_bytes);
-  CUtensorMap km, vm, kp, vp;
+  CUtensorMap qm, km, vm, kp, vp;
   const int64_t page_rows = (int64_t)a.n_pages * a.H * a.page_size;
-  bool ok = tma_map_sw128_bf16(&kp, a.k_pages, D, 1, page_rows, 1, a.page_size) &&
+  bool ok = tma_map_sw128_bf16(&qm, a.q, D, a.Hq, a.n_tok, a.G, p.tile_tok) &&
+            tma_map_sw128_bf16(&kp, a.k_pages, D, 1, page_rows, 1, a.page_size) &&
             tma_map_sw128_bf16(&vp, a.v_pages, D, 1, page_rows, 1, a.page_size);
   if (a.m_cap > 0)
     ok = ok && tma_map_sw128_bf16(&km, a.k_mem, D, a.H, (int64_t)a.B * a.m_cap, 1, kMemRows) &&
@@ -862,8 +944,8 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   auto kern = tree_tc_kernel<D, kQT>;
   if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)p.smem)) return rc;
   const unsigned grid = (unsigned)num_sms();
-  if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, km, vm, kp, vp, a,
-                          p.part_rows, p.q_rows, p.n_k, p.n_v, part_o, part_ml, cuts))
+  if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, qm, km, vm, kp, vp, a,
+                          p.part_rows, p.tile_tok * a.G, p.q_rows, p.n_k, p.n_v, part_o, part_ml, cuts))
     return rc;
   return tree_merge_launch(a, D, (int)grid, 1, p.part_rows, part_o, part_ml, cuts, s);
 }
