@@ -12,10 +12,18 @@
 // Queries and cached keys are already rotated (msa_paged_append); memory
 // rows keep their document-wise rotation.
 //
-// This file holds the CUDA-core kernel -- one CTA per (split of a
-// sequence's keys, 16 query rows = tokens x heads of a KV group, KV head),
-// 32-key tiles in shared memory in fp32, one pass with a running maximum and
-// sum -- the kernel that joins the splits, and the entry point.
+// This file holds the fp32 kernels and the entry point; bf16 goes to
+// tree_attn_few.cu and tree_attn_tc.cu.  fp32 stays on the CUDA cores (the
+// tensor cores would round the operands): 4 D operations a row and key at
+// four bytes, bound by the fp32 pipe and shared memory for many rows and by
+// latency for the small calls fp32 is used for.  One CTA per (split of a
+// sequence's keys, 4 RW query rows = tokens x heads of a KV group, KV head):
+// 32-key tiles, a key a lane, two in shared memory (the next tile is copied
+// while this one is used), RW rows a warp so that a key read from shared
+// memory serves all of them, one pass with a running maximum and sum; a
+// second launch joins the splits.  (2 sequences of up to 16 tokens over 322
+// keys: 42 us with scalar loads of one tile and 64 keys a split; this
+// UNMEASURED us.)
 #include <algorithm>
 #include <cmath>
 
@@ -25,27 +33,32 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 16;   // query rows of a CTA
 constexpr int kTile = 32;   // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct TreePlan {
-  int n_blk, n_split;
+  int rw, n_blk, n_split;
   size_t po_bytes, ml_bytes, total;
 };
 
-// Splits: enough CTAs to cover the SMs twice, each of at least 64 keys of
-// the longest sequence the buffers can hold, at most 64.
+// Splits: enough CTAs to cover the SMs twice, each of at least one tile of
+// the longest sequence the buffers can hold, at most 64.  Rows of a warp: the
+// fewest that cover a sequence's rows, 8 at most (a key read from shared
+// memory then serves 8), and fewer while even the most splits leave SMs empty.
 TreePlan tree_plan(int B, int n_max, int Hq, int H, int D, int m_cap, int max_pages,
                    int page_size) {
   TreePlan p{};
-  p.n_blk = (n_max * (Hq / H) + kRows - 1) / kRows;
-  const int64_t base = (int64_t)B * H * p.n_blk;
+  const int rows_kv = n_max * (Hq / H);
   const int64_t keys = (int64_t)m_cap + (int64_t)max_pages * page_size;
+  const int64_t most = std::min<int64_t>((keys + kTile - 1) / kTile, 64);
   const int64_t want = 2LL * num_sms();
-  int64_t ns = (want + base - 1) / base;
-  ns = std::min<int64_t>({ns, (keys + 63) / 64, 64});
-  p.n_split = (int)std::max<int64_t>(1, ns);
+  p.rw = rows_kv <= 4 ? 1 : rows_kv <= 8 ? 2 : rows_kv <= 16 ? 4 : 8;
+  for (;; p.rw /= 2) {
+    p.n_blk = (rows_kv + 4 * p.rw - 1) / (4 * p.rw);
+    const int64_t base = (int64_t)B * H * p.n_blk;
+    p.n_split = (int)std::max<int64_t>(1, std::min((want + base - 1) / base, most));
+    if (p.rw == 1 || base * p.n_split >= num_sms()) break;
+  }
   const size_t rows = (size_t)B * n_max * Hq;
   if (p.n_split > 1) {
     p.po_bytes = round_up(rows * p.n_split * D * sizeof(float), 256);
@@ -55,16 +68,29 @@ TreePlan tree_plan(int B, int n_max, int Hq, int H, int D, int m_cap, int max_pa
   return p;
 }
 
-template <typename T, int D>
+template <int D, int RW> struct SimtSmem {
+  float ks[2][kTile][D + 4];  // padded: a quarter warp's 16-byte reads of 8 rows
+  float vs[2][kTile][D];
+  float qs[4 * RW][D];
+  float ps[4 * RW][kTile];
+  TreeMask mask;
+};
+
+// 16 bytes into shared memory, zeros where `live` is false.
+__device__ __forceinline__ void cp16_or_zero(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+
+template <int D, int RW>
 __global__ void __launch_bounds__(kThreads)
 tree_simt_kernel(const __grid_constant__ TreeArgs a, int n_split, float* __restrict__ part_o,
                  float2* __restrict__ part_ml) {
   constexpr int PER = D / 32;
-  constexpr int MAXR = kRows / (kThreads / 32);  // query rows a warp
-  __shared__ float qs[kRows][D];
-  __shared__ float ks[kTile][D + 1];
-  __shared__ float vs[kTile][D];
-  __shared__ TreeMask mask;
+  extern __shared__ __align__(16) unsigned char simt_raw[];
+  SimtSmem<D, RW>& sm = *reinterpret_cast<SimtSmem<D, RW>*>(simt_raw);
   pdl_trigger();
   pdl_wait();
   const int split = blockIdx.x, blk = blockIdx.y;
@@ -73,162 +99,233 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int n_split, float* __restr
   const TreeSeq s = tree_seq(a, b);
   if (s.error && tid == 0) record_error(a.status, s.error);
   const int G = a.G;
-  const int row0 = blk * kRows;
-  const int rows = min(kRows, s.n * G - row0);
+  const int row0 = blk * 4 * RW;
+  const int rows = min(4 * RW, s.n * G - row0);
   if (rows <= 0) return;
-  tree_mask(a, s, mask, tid, [] { __syncthreads(); });
 
-  for (int e = tid; e < rows * D; e += kThreads) {
-    const int r = row0 + e / D, d = e % D;
-    const int64_t off = ((s.t0 + r / G) * a.Hq + g * G + r % G) * D + d;
-    qs[e / D][d] = Elem<T>::to_f(static_cast<const T*>(a.q)[off]) * a.qscale;
-  }
   const int keys = s.M + s.cache;
   const int tiles = (keys + kTile - 1) / kTile;
-  const int k_lo = (int)((int64_t)split * tiles / n_split) * kTile;
-  const int k_hi = min(keys, (int)((int64_t)(split + 1) * tiles / n_split) * kTile);
-
-  float m_run[MAXR], l_run[MAXR], o[MAXR][PER];
-  uint4 anc[MAXR];
-  bool alive[MAXR];
-#pragma unroll
-  for (int rr = 0; rr < MAXR; ++rr) {
-    m_run[rr] = -INFINITY;
-    l_run[rr] = 0.f;
-#pragma unroll
-    for (int x = 0; x < PER; ++x) o[rr][x] = 0.f;
-    const int r = warp + 4 * rr;
-    const int tok = r < rows ? (row0 + r) / G : 0;
-    anc[rr] = mask.anc[tok];
-    alive[rr] = r < rows && mask.up[tok] != kTreeDead;
-  }
-
-  for (int t0 = k_lo; t0 < k_hi; t0 += kTile) {
-    __syncthreads();
-    for (int e = tid; e < kTile * D; e += kThreads) {
-      const int j = e / D, d = e % D;
-      const int kk = t0 + j;
-      float kv = 0.f, vv = 0.f;
-      if (kk < k_hi) {
+  const int t_lo = (int)((int64_t)split * tiles / n_split);
+  const int t_hi = (int)((int64_t)(split + 1) * tiles / n_split);
+  // Copies tile t into buffer t & 1: four threads a key; keys past the end
+  // and on pages that are not there read as zeros.
+  auto copy = [&](int t) {
+    if (t < t_hi) {
+      const int j = tid >> 2, kk = t * kTile + j, d0 = (tid & 3) * 4;
+      const float *kp = static_cast<const float*>(a.k_pages),
+                  *vp = static_cast<const float*>(a.v_pages);
+      bool live = kk < keys;
+      if (live) {
+        int64_t off;
         if (kk < s.M) {
-          const int64_t off = (((int64_t)b * a.m_cap + kk) * a.H + g) * D + d;
-          kv = Elem<T>::to_f(static_cast<const T*>(a.k_mem)[off]);
-          vv = Elem<T>::to_f(static_cast<const T*>(a.v_mem)[off]);
+          kp = static_cast<const float*>(a.k_mem);
+          vp = static_cast<const float*>(a.v_mem);
+          off = (((int64_t)b * a.m_cap + kk) * a.H + g) * D;
         } else {
           const int slot = kk - s.M;
           const int pg = a.block_table[(int64_t)b * a.max_pages + slot / a.page_size];
-          if (pg >= 0 && pg < a.n_pages) {
-            const int64_t off =
-                (((int64_t)pg * a.H + g) * a.page_size + slot % a.page_size) * D + d;
-            kv = Elem<T>::to_f(static_cast<const T*>(a.k_pages)[off]);
-            vv = Elem<T>::to_f(static_cast<const T*>(a.v_pages)[off]);
-          } else if (d == 0) {
-            record_error(a.status, MSA_ERR_INVALID_ARG);
-          }
+          live = pg >= 0 && pg < a.n_pages;
+          if (!live && (tid & 3) == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
+          off = live ? (((int64_t)pg * a.H + g) * a.page_size + slot % a.page_size) * D : 0;
         }
+        kp += off;
+        vp += off;
       }
-      ks[j][d] = kv;
-      vs[j][d] = vv;
+#pragma unroll
+      for (int d = 0; d < D; d += 16) {
+        cp16_or_zero(&sm.ks[t & 1][j][d + d0], kp + d + d0, live);
+        cp16_or_zero(&sm.vs[t & 1][j][d + d0], vp + d + d0, live);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  copy(t_lo);
+  for (int e = tid; e < 4 * RW * (D / 4); e += kThreads) {
+    const int i = e / (D / 4), d = e % (D / 4) * 4, r = row0 + i;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < rows)
+      q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                           ((s.t0 + r / G) * a.Hq + g * G + r % G) * D + d);
+    *reinterpret_cast<float4*>(&sm.qs[i][d]) =
+        make_float4(q.x * a.qscale, q.y * a.qscale, q.z * a.qscale, q.w * a.qscale);
+  }
+  tree_mask(a, s, sm.mask, tid, [] { __syncthreads(); });
+
+  float m_run[RW], l_part[RW], o[RW][PER];
+  int tok[RW];
+  bool alive[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    m_run[i] = -INFINITY;
+    l_part[i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) o[i][x] = 0.f;
+    const int r = warp * RW + i;
+    tok[i] = r < rows ? (row0 + r) / G : 0;
+    alive[i] = r < rows && sm.mask.up[tok[i]] != kTreeDead;
+  }
+
+  for (int t = t_lo; t < t_hi; ++t) {
+    copy(t + 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    const int kk = t0 + lane;
+    const float (*ks)[D + 4] = sm.ks[t & 1];
+    const float (*vs)[D] = sm.vs[t & 1];
+    float sc[RW];
 #pragma unroll
-    for (int rr = 0; rr < MAXR; ++rr) {
-      const int r = warp + 4 * rr;
-      if (r >= rows) break;  // warp-uniform
-      float sc = 0.f;
-#pragma unroll 8
-      for (int d = 0; d < D; ++d) sc = fmaf(qs[r][d], ks[lane][d], sc);
-      const int j = kk - s.M - s.L;  // drafted token, if >= 0
-      const bool ok = alive[rr] && kk < k_hi && (j < 0 || tree_bit(anc[rr], j));
-      sc = ok ? sc : -INFINITY;
-      float mt = sc;
+    for (int i = 0; i < RW; ++i) sc[i] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      const float4 k = *reinterpret_cast<const float4*>(&ks[lane][d]);
 #pragma unroll
-      for (int off = 16; off; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+      for (int i = 0; i < RW; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(&sm.qs[warp * RW + i][d]);
+        sc[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, sc[i]))));
+      }
+    }
+    const int kk = t * kTile + lane, j = kk - s.M - s.L;  // j >= 0: drafted token
+    // every alive row sees every key
+    const bool all = (t + 1) * kTile <= s.M + s.L;
+    uint32_t seen[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const bool ok =
+          all || (kk < keys && (j < 0 || tree_bit(sm.mask.anc[tok[i]], j)));
+      seen[i] = all ? 0xffffffffu : __ballot_sync(0xffffffffu, ok);
+      sc[i] = ok ? sc[i] : -INFINITY;
+      float mt = sc[i];
+#pragma unroll
+      for (int x = 16; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
       // (a NaN score is no maximum: it makes its own weight NaN; a score of
       // -inf weighs nothing even while no other was seen)
-      const float m_new = fmaxf(m_run[rr], mt);
+      const float m_new = fmaxf(m_run[i], mt);
       const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float p = exp2f(sc - ref);
-      const float corr = exp2f(m_run[rr] - ref);
-      float ps = p;
+      const float p = exp2f(sc[i] - ref);
+      const float corr = exp2f(m_run[i] - ref);
+      l_part[i] = l_part[i] * corr + p;
+      m_run[i] = m_new;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-      l_run[rr] = l_run[rr] * corr + ps;
-      m_run[rr] = m_new;
+      for (int x = 0; x < PER; ++x) o[i][x] *= corr;
+      sm.ps[warp * RW + i][lane] = p;
+    }
+    __syncwarp();
+    // (seen keys only: a masked value, NaN included, adds nothing)
+#pragma unroll 2
+    for (int k = 0; k < kTile; k += 4) {
+      float v[4][PER];
 #pragma unroll
-      for (int x = 0; x < PER; ++x) o[rr][x] *= corr;
-      // seen keys only: a masked value, NaN included, adds nothing
-      for (uint32_t seen = __ballot_sync(0xffffffffu, ok); seen; seen &= seen - 1) {
-        const int i = __ffs(seen) - 1;
-        const float pi = __shfl_sync(0xffffffffu, p, i);
+      for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int x = 0; x < PER; ++x) o[rr][x] = fmaf(pi, vs[i][lane + 32 * x], o[rr][x]);
+        for (int x = 0; x < PER; ++x) v[y][x] = vs[k + y][lane + 32 * x];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const float4 p4 = *reinterpret_cast<const float4*>(&sm.ps[warp * RW + i][k]);
+        const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+        const uint32_t bits = seen[i] >> k;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (bits & (1u << y)) {
+#pragma unroll
+            for (int x = 0; x < PER; ++x) o[i][x] = fmaf(p[y], v[y][x], o[i][x]);
+          }
       }
     }
+    __syncthreads();  // the buffer may be copied into again
   }
 
 #pragma unroll
-  for (int rr = 0; rr < MAXR; ++rr) {
-    const int r = warp + 4 * rr;
+  for (int i = 0; i < RW; ++i) {
+    const int r = warp * RW + i;
     if (r >= rows) break;
-    const int tok = (row0 + r) / G, hq = g * G + (row0 + r) % G;
+    float l = l_part[i];
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (!alive[i]) l = 0.f;  // pruned: weighs nothing
+    const int hq = g * G + (row0 + r) % G;
     if (n_split == 1) {
       // no weight at all: zero; a NaN sum stays NaN
-      const float inv = l_run[rr] == 0.f ? 0.f : 1.f / l_run[rr];
-      T* op = static_cast<T*>(a.out) + ((s.t0 + tok) * a.Hq + hq) * D;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float* op = static_cast<float*>(a.out) + ((s.t0 + tok[i]) * a.Hq + hq) * D;
 #pragma unroll
-      for (int x = 0; x < PER; ++x)
-        op[lane + 32 * x] = Elem<T>::from_f(l_run[rr] == 0.f ? 0.f : o[rr][x] * inv);
+      for (int x = 0; x < PER; ++x) op[lane + 32 * x] = l == 0.f ? 0.f : o[i][x] * inv;
     } else {
-      const int64_t row = ((int64_t)b * a.n_max + tok) * a.Hq + hq;
+      const int64_t row = ((int64_t)b * a.n_max + tok[i]) * a.Hq + hq;
       float* po = part_o + (row * n_split + split) * D;
 #pragma unroll
-      for (int x = 0; x < PER; ++x) po[lane + 32 * x] = o[rr][x];
-      if (lane == 0) part_ml[row * n_split + split] = make_float2(m_run[rr], l_run[rr]);
+      for (int x = 0; x < PER; ++x) po[lane + 32 * x] = o[i][x];
+      if (lane == 0) part_ml[row * n_split + split] = make_float2(m_run[i], l);
     }
   }
 }
 
 // Joins the key splits of one (token, head) row.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(D)
 tree_combine_kernel(const __grid_constant__ TreeArgs a, int n_split,
                     const float* __restrict__ part_o, const float2* __restrict__ part_ml) {
+  __shared__ float w[64];
   pdl_trigger();
   pdl_wait();
   const int hq = blockIdx.x % a.Hq;
   const int i = blockIdx.x / a.Hq % a.n_max, b = blockIdx.x / a.Hq / a.n_max;
+  const int64_t row = ((int64_t)b * a.n_max + i) * a.Hq + hq;
+  const int tid = threadIdx.x, lane = tid & 31;
   const TreeSeq s = tree_seq(a, b);
   if (i >= s.n) return;
-  const int64_t row = ((int64_t)b * a.n_max + i) * a.Hq + hq;
-  const float2* ml = part_ml + row * n_split;
-  float m = -INFINITY;
-  for (int sp = 0; sp < n_split; ++sp) m = fmaxf(m, ml[sp].x);
-  float l = 0.f, acc = 0.f;
-  for (int sp = 0; sp < n_split; ++sp) {
-    if (ml[sp].y == 0.f) continue;
-    const float w = m == -INFINITY ? 1.f : exp2f(ml[sp].x - m);
-    l += w * ml[sp].y;
-    acc += w * part_o[(row * n_split + sp) * D + threadIdx.x];
+  // every warp finds the weights of all splits, two a lane (n_split <= 64)
+  float2 ml[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    ml[h] = make_float2(-INFINITY, 0.f);
+    if (lane + 32 * h < n_split) ml[h] = part_ml[row * n_split + lane + 32 * h];
   }
-  static_cast<T*>(a.out)[((s.t0 + i) * a.Hq + hq) * D + threadIdx.x] =
-      Elem<T>::from_f(l == 0.f ? 0.f : acc / l);
+  float m = fmaxf(ml[0].y == 0.f ? -INFINITY : ml[0].x, ml[1].y == 0.f ? -INFINITY : ml[1].x);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float l = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    // (a split without weight is left out: its O may hold NaN)
+    const float wt =
+        ml[h].y == 0.f ? 0.f : m == -INFINITY ? 1.f : exp2f(ml[h].x - m);
+    if (ml[h].y != 0.f) l += wt * ml[h].y;
+    if (tid < 32) w[lane + 32 * h] = wt;
+  }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  __syncthreads();
+  float acc = 0.f;
+#pragma unroll 8
+  for (int sp = 0; sp < n_split; ++sp) {
+    const float v = part_o[(row * n_split + sp) * D + tid];
+    if (w[sp] != 0.f) acc = fmaf(w[sp], v, acc);
+  }
+  static_cast<float*>(a.out)[((s.t0 + i) * a.Hq + hq) * D + tid] = l == 0.f ? 0.f : acc / l;
 }
 
-template <typename T, int D>
+template <int D, int RW>
 int launch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s) {
   float* part_o = static_cast<float*>(ws);
   float2* part_ml =
       reinterpret_cast<float2*>(static_cast<unsigned char*>(ws) + p.po_bytes);
   const dim3 grid((unsigned)p.n_split, (unsigned)p.n_blk, (unsigned)(a.B * a.H));
-  if (int rc = launch_pdl(tree_simt_kernel<T, D>, grid, dim3(kThreads), 0, s, a, p.n_split,
-                          part_o, part_ml))
+  constexpr int kSmem = (int)sizeof(SimtSmem<D, RW>);
+  auto kern = tree_simt_kernel<D, RW>;
+  if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmem)) return rc;
+  if (int rc = launch_pdl(kern, grid, dim3(kThreads), kSmem, s, a, p.n_split, part_o, part_ml))
     return rc;
   if (p.n_split == 1) return MSA_OK;
-  return launch_pdl(tree_combine_kernel<T, D>, dim3((unsigned)((int64_t)a.B * a.n_max * a.Hq)),
+  return launch_pdl(tree_combine_kernel<D>, dim3((unsigned)((int64_t)a.B * a.n_max * a.Hq)),
                     dim3(D), 0, s, a, p.n_split, static_cast<const float*>(part_o),
                     static_cast<const float2*>(part_ml));
+}
+
+template <int D>
+int dispatch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s) {
+  return p.rw == 1   ? launch_simt<D, 1>(a, p, ws, s)
+         : p.rw == 2 ? launch_simt<D, 2>(a, p, ws, s)
+         : p.rw == 4 ? launch_simt<D, 4>(a, p, ws, s)
+                     : launch_simt<D, 8>(a, p, ws, s);
 }
 
 // Shape checks shared by the call and its workspace size; a MSA status.
@@ -300,7 +397,7 @@ int tree_body(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int 
   if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MSA_ERR_WORKSPACE;
   if (dt == MSA_BF16)
     return few ? tree_few_launch(a, D, ws, s) : tree_tc_launch(a, D, ws, s);
-  return D == 64 ? launch_simt<float, 64>(a, p, ws, s) : launch_simt<float, 128>(a, p, ws, s);
+  return D == 64 ? dispatch_simt<64>(a, p, ws, s) : dispatch_simt<128>(a, p, ws, s);
 }
 
 }  // namespace
