@@ -145,9 +145,22 @@ def _th():
     return _torch
 
 
+def _device() -> int:
+    """The current CUDA device, without torch's checks for an uninitialised
+    CUDA (-2, no tensor's device, where there is none)."""
+    try:
+        return _th()._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return -2
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return _th().cuda.current_stream().cuda_stream
+        torch = _th()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch._C._cuda_getDevice())  # the same handle, 3 us sooner
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -196,7 +209,7 @@ def _device_ok(t, host_ok: bool) -> bool:
     """A tensor the kernels may read: on the current CUDA device, or (where
     the call reads a tiered bank over the host link) in pinned host memory."""
     if t.is_cuda:  # CUDA is up then: its current device without the checks for that
-        return t.get_device() == _th()._C._cuda_getDevice()
+        return t.get_device() == _device()
     return host_ok and t.is_pinned()
 
 
@@ -222,30 +235,32 @@ def _numel_ok(t, n, what, kind=None, host_ok=False):
                          f"the kernels read it from {where}")
 
 
-def _arg(t, n, what, kind):
-    """The address of a tensor argument that passes _numel_ok."""
+def _arg(t, n, what, kind, dev):
+    """The address of a tensor argument that passes _numel_ok; dev is
+    _device()."""
     if t is None or isinstance(t, int):
         return t
-    if (t.dtype is not _torch_dtype(kind) or t.numel() < n or not t.is_contiguous()
-            or not _device_ok(t, False)):
+    if (t.get_device() != dev or t.dtype is not _torch_dtype(kind) or t.numel() < n
+            or not t.is_contiguous()):
         _numel_ok(t, n, what, kind)  # says what is wrong with it
     return t.data_ptr()
 
 
-def _rows_ok(t, n, heads, D, what, kind) -> int:
-    """Checks an operand of n tokens of [heads][D] whose tokens may lie apart
-    (a slice of a fused projection's output): each token's heads contiguous,
-    the tokens a fixed, 16-byte multiple of elements apart.  Returns that
-    stride (heads * D for a raw address, None or an empty tensor)."""
+def _rows(t, n, heads, D, what, kind, dev):
+    """The address of an operand of n tokens of [heads][D] and the elements
+    from token to token: the tokens may lie apart (a slice of a fused
+    projection's output), each token's heads contiguous and the tokens a
+    16-byte multiple apart.  (Raw addresses, None and empty tensors are
+    dense.)"""
+    stride = heads * D
     if t is None or isinstance(t, int):
-        return heads * D
+        return t, stride
     want = _torch_dtype(kind)
-    if want is not None and t.dtype != want:
+    if want is not None and t.dtype is not want:
         raise ValueError(f"{what} is {t.dtype}, the call reads {want}")
     shape = t.shape
     if len(shape) != 3 or shape[0] < n or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{what} has shape {tuple(shape)}, needs [>= {n}, {heads}, {D}]")
-    stride = heads * D
     if shape[0] > 0 and heads > 0:
         s0, s1, s2 = t.stride()
         if s2 != 1 or (heads > 1 and s1 != D):
@@ -255,9 +270,9 @@ def _rows_ok(t, n, heads, D, what, kind) -> int:
                 raise ValueError(f"{what}: tokens must be a multiple of 16 bytes apart, and not "
                                  f"overlap (stride {s0} elements)")
             stride = s0
-    if not _device_ok(t, False):
+    if t.get_device() != dev and not _device_ok(t, False):
         raise ValueError(f"{what} is on {t.device}; it must be on the current CUDA device")
-    return stride
+    return t.data_ptr(), stride
 
 
 def _ws_ok(ws, ws_bytes):
@@ -514,14 +529,14 @@ def msa_qk_norm_rope(dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, e
                      q_out, k_out, stream=None):
     """q and k: [n_tok][heads][D] tensors, the token strides taken from them
     (raw addresses are dense)."""
-    es = _es(dt)
-    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
-    ks = _rows_ok(k, n_tok, H, D, "k", es)
+    es, dev = _es(dt), _device()
+    qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
+    kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
     _check("msa_qk_norm_rope", lib().msa_qk_norm_rope(
-        dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _arg(q_weight, D, "q_weight", es),
-        _arg(k_weight, D, "k_weight", es), _arg(positions, n_tok, "positions", I32), eps,
-        rope_base, _arg(q_out, n_tok * Hq * D, "q_out", es),
-        _arg(k_out, n_tok * H * D, "k_out", es), _stream(stream)))
+        dt, n_tok, Hq, H, D, qp, qs, kp, ks, _arg(q_weight, D, "q_weight", es, dev),
+        _arg(k_weight, D, "k_weight", es, dev), _arg(positions, n_tok, "positions", I32, dev), eps,
+        rope_base, _arg(q_out, n_tok * Hq * D, "q_out", es, dev),
+        _arg(k_out, n_tok * H * D, "k_out", es, dev), _stream(stream)))
 
 
 def msa_qk_norm_rope_backward_workspace_size(n_tok, D) -> int:
@@ -533,19 +548,20 @@ def msa_qk_norm_rope_backward(dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_we
                               ws_bytes, stream=None):
     """q, k, dq and dk: [n_tok][heads][D] tensors, the token strides taken
     from them (raw addresses are dense)."""
-    es, gs = _es(dt), _es(grad_dt)
-    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
-    ks = _rows_ok(k, n_tok, H, D, "k", es)
-    dqs = _rows_ok(dq, n_tok, Hq, D, "dq", gs)
-    dks = _rows_ok(dk, n_tok, H, D, "dk", gs)
+    es, gs, dev = _es(dt), _es(grad_dt), _device()
+    qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
+    kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
+    dqp, dqs = _rows(dq, n_tok, Hq, D, "dq", gs, dev)
+    dkp, dks = _rows(dk, n_tok, H, D, "dk", gs, dev)
     _ws_ok(ws, ws_bytes)
     _check("msa_qk_norm_rope_backward", lib().msa_qk_norm_rope_backward(
-        dt, grad_dt, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks,
-        _arg(q_weight, D, "q_weight", es), _arg(k_weight, D, "k_weight", es),
-        _arg(positions, n_tok, "positions", I32), eps, rope_base,
-        _arg(dq_out, n_tok * Hq * D, "dq_out", gs), _arg(dk_out, n_tok * H * D, "dk_out", gs),
-        _ptr(dq), dqs, _ptr(dk), dks, _arg(dq_weight, D, "dq_weight", F32),
-        _arg(dk_weight, D, "dk_weight", F32), _ptr(ws), ws_bytes, _stream(stream)))
+        dt, grad_dt, n_tok, Hq, H, D, qp, qs, kp, ks,
+        _arg(q_weight, D, "q_weight", es, dev), _arg(k_weight, D, "k_weight", es, dev),
+        _arg(positions, n_tok, "positions", I32, dev), eps, rope_base,
+        _arg(dq_out, n_tok * Hq * D, "dq_out", gs, dev),
+        _arg(dk_out, n_tok * H * D, "dk_out", gs, dev), dqp, dqs, dkp, dks,
+        _arg(dq_weight, D, "dq_weight", F32, dev),
+        _arg(dk_weight, D, "dk_weight", F32, dev), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_offsets, positions,
@@ -553,19 +569,20 @@ def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_of
                      k_pages, v_pages, q_out, stream=None):
     """q, k and v: [n_tok][heads][D] tensors, the token strides taken from
     them (raw addresses are dense)."""
-    es = _es(dt)
-    qs = _rows_ok(q, n_tok, Hq, D, "q", es)
-    ks = _rows_ok(k, n_tok, H, D, "k", es)
-    vs = _rows_ok(v, n_tok, H, D, "v", es)
+    es, dev = _es(dt), _device()
+    qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
+    kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
+    vp, vs = _rows(v, n_tok, H, D, "v", es, dev)
     pool = n_pages * H * page_size * D
     _check("msa_paged_append", lib().msa_paged_append(
-        dt, B, n_tok, Hq, H, D, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-        _arg(q_weight, D, "q_weight", es), _arg(k_weight, D, "k_weight", es),
-        _arg(tok_offsets, B + 1, "tok_offsets", I64), _arg(positions, n_tok, "positions", I32),
-        eps, rope_base, _arg(block_table, B * max_pages, "block_table", I32), max_pages,
-        _arg(cache_len, B, "cache_len", I32), page_size, n_pages,
-        _arg(k_pages, pool, "k_pages", es), _arg(v_pages, pool, "v_pages", es),
-        _arg(q_out, n_tok * Hq * D, "q_out", es), _stream(stream)))
+        dt, B, n_tok, Hq, H, D, qp, qs, kp, ks, vp, vs,
+        _arg(q_weight, D, "q_weight", es, dev), _arg(k_weight, D, "k_weight", es, dev),
+        _arg(tok_offsets, B + 1, "tok_offsets", I64, dev),
+        _arg(positions, n_tok, "positions", I32, dev),
+        eps, rope_base, _arg(block_table, B * max_pages, "block_table", I32, dev), max_pages,
+        _arg(cache_len, B, "cache_len", I32, dev), page_size, n_pages,
+        _arg(k_pages, pool, "k_pages", es, dev), _arg(v_pages, pool, "v_pages", es, dev),
+        _arg(q_out, n_tok * Hq * D, "q_out", es, dev), _stream(stream)))
 
 
 def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size) -> int:
@@ -575,15 +592,16 @@ def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_
 def msa_tree_attn(dt, B, n_tok, n_max, Hq, H, D, q, tok_offsets, parents, k_mem, v_mem, mem_len,
                   m_cap, k_pages, v_pages, n_pages, page_size, block_table, max_pages, cache_len,
                   scale, out, ws, ws_bytes, stream=None):
-    es = _es(dt)
+    es, dev = _es(dt), _device()
     rows, mem, pool = n_tok * Hq * D, B * m_cap * H * D, n_pages * H * page_size * D
     _ws_ok(ws, ws_bytes)
     _check("msa_tree_attn", lib().msa_tree_attn(
-        dt, B, n_tok, n_max, Hq, H, D, _arg(q, rows, "q", es),
-        _arg(tok_offsets, B + 1, "tok_offsets", I64), _arg(parents, n_tok, "parents", I32),
-        _arg(k_mem, mem, "k_mem", es), _arg(v_mem, mem, "v_mem", es),
-        _arg(mem_len, B if m_cap else 0, "mem_len", I32), m_cap,
-        _arg(k_pages, pool, "k_pages", es), _arg(v_pages, pool, "v_pages", es), n_pages,
-        page_size, _arg(block_table, B * max_pages, "block_table", I32), max_pages,
-        _arg(cache_len, B, "cache_len", I32), scale, _arg(out, rows, "out", es), _ptr(ws),
+        dt, B, n_tok, n_max, Hq, H, D, _arg(q, rows, "q", es, dev),
+        _arg(tok_offsets, B + 1, "tok_offsets", I64, dev),
+        _arg(parents, n_tok, "parents", I32, dev),
+        _arg(k_mem, mem, "k_mem", es, dev), _arg(v_mem, mem, "v_mem", es, dev),
+        _arg(mem_len, B if m_cap else 0, "mem_len", I32, dev), m_cap,
+        _arg(k_pages, pool, "k_pages", es, dev), _arg(v_pages, pool, "v_pages", es, dev), n_pages,
+        page_size, _arg(block_table, B * max_pages, "block_table", I32, dev), max_pages,
+        _arg(cache_len, B, "cache_len", I32, dev), scale, _arg(out, rows, "out", es, dev), _ptr(ws),
         ws_bytes, _stream(stream)))

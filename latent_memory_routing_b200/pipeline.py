@@ -339,7 +339,7 @@ def _heads(t):
 
 def _dense(t):
     """An uninitialised contiguous tensor like t (None for None)."""
-    return None if t is None else t.new_empty(t.shape)
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
