@@ -154,7 +154,7 @@ int tree_merge_launch(const TreeArgs& a, int D, int ctas, int per, int part_rows
                       const float* part_o, const float2* part_ml, const TreeCut* cuts,
                       cudaStream_t s);
 
-// bf16, n_max G <= 32 rows a KV head: a warp a worker (tree_attn_few.cu).
+// bf16, n_max G <= 16 rows a KV head: a warp a worker (tree_attn_few.cu).
 bool tree_few_takes(int n_max, int G);
 size_t tree_few_workspace_size(int n_max, int G, int D);
 int tree_few_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);

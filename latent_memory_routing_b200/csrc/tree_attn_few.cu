@@ -1,6 +1,6 @@
 // bf16 attention for drafted token trees over [memory ; paged cache ; drafted
 // tokens] when a KV head has few query rows (method and semantics:
-// tree_attn.cu): plain decode and small trees, R = n G <= 32 rows.
+// tree_attn.cu): plain decode and small trees, R = n G <= 16 rows.
 //
 // Mathematics.  As tree_attn_tc.cu: S = Q K^T, p = 2^(scale log2(e) s - m),
 // O += bf16(p) V, l += p, one pass over the keys.
@@ -17,10 +17,10 @@
 //   * A warp's lane 0 copies slices of K and V by TMA into the warp's own ring
 //     (a slice never crosses a page: pages hold a multiple of 16 rows), waits
 //     on its own barriers, and no warp waits for another.
-//   * A slice is 16 x 16 of S and 16 x D of O per 16 rows on the warp-level
+//   * A slice is 16 x 16 of S and 16 x D of O on the warp-level
 //     tensor instructions (m16n8k16): the accumulators stay in registers and
 //     P's fragment is S's.  Their rate is no limit: a slice's 64 instructions
-//     a row tile against the 8 KB that its SM receives in 350 cycles.
+//     against the 8 KB that its SM receives in 350 cycles.
 //   * In a slice that reaches past the sequence's rows or into its drafted
 //     rows, unseen scores become -inf, V rows past the end zero, and
 //     non-finite drafted values are taken out of V (0 times them would reach
@@ -41,7 +41,7 @@ constexpr int kFewThreads = 32 * kWarps;
 constexpr int kMinRange = 6;
 constexpr float kRescaleLog2 = 8.f;
 
-template <int D, int MT> struct FC {
+template <int D> struct FC {
   static constexpr int KB = D / 64;                 // 64-dim blocks of a slice
   static constexpr int BLK = kSlice * 128;          // 2 KB
   static constexpr int SLICE = 2 * KB * BLK;        // K and V of a slice
@@ -49,11 +49,11 @@ template <int D, int MT> struct FC {
   static constexpr size_t SMEM = 1024 + (size_t)kWarps * DEPTH * SLICE;
 };
 
-template <int MT> struct FewAux {
+struct FewAux {
   int64_t pre[kFewThreads + 1];          // slices before each thread's sequences
   TreeSeq seq[kFewThreads];              // the sequences, where a thread has one at most
   uint64_t full[kWarps][6];              // ring slots (DEPTH <= 6)
-  uint4 anc[kWarps][16 * MT];            // what each row's token sees of its tree
+  uint32_t anc[kWarps][16];           // what each row's token sees of its tree
   signed char par[kWarps][128];
 };
 
@@ -113,7 +113,7 @@ struct Cursor {
   }
 };
 
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(kFewThreads, 1)
 tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                 const __grid_constant__ CUtensorMap tm_vm,
@@ -121,11 +121,11 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ TreeArgs a,
                 int part_rows, float* __restrict__ part_o, float2* __restrict__ part_ml,
                 TreeCut* __restrict__ cuts) {
-  using C = FC<D, MT>;
+  using C = FC<D>;
   pdl_trigger();  // the merge: its blocks come as this grid's leave
   pdl_wait();
   extern __shared__ __align__(1024) unsigned char dsm[];
-  __shared__ FewAux<MT> aux;
+  __shared__ FewAux aux;
   unsigned char* base = tc::smem_align<1024>(dsm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* ring = base + warp * C::DEPTH * C::SLICE;
@@ -290,22 +290,19 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     const int rows = s.n * a.G, n_ms = slices(s.M);
     const int cnt = (int)min((int64_t)(cu.nt - cu.j), cu.left), j_lo = cu.j;
     const int part = j_lo > 0 ? 0 : cnt < cu.nt ? 1 : -1;
-    uint32_t qf[MT][D / 16][4];
-    int64_t out_row[MT][2];
+    uint32_t qf[D / 16][4];
+    int64_t out_row[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int h = 0; h < 2; ++h) {
+      const int r = r4 + 8 * h;
+      out_row[h] = r < rows ? (s.t0 + r / a.G) * a.Hq + cu.g * a.G + r % a.G : (int64_t)-1;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + out_row[h] * D + c2;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = mt * 16 + r4 + 8 * h;
-        out_row[mt][h] =
-            r < rows ? (s.t0 + r / a.G) * a.Hq + cu.g * a.G + r % a.G : (int64_t)-1;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + out_row[mt][h] * D + c2;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          qf[mt][kk][h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16) : 0u;
-          qf[mt][kk][2 + h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 8) : 0u;
-        }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16) : 0u;
+        qf[kk][2 + h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 8) : 0u;
       }
+    }
     // ancestor sets, a lane a row
     __syncwarp();
     if (a.parents) {
@@ -319,7 +316,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       }
       __syncwarp();
     }
-    if (lane < rows) {  // rows <= 32, tokens <= 32
+    if (lane < rows) {  // at most 16 rows, so at most 16 tokens
       uint32_t m = 0;
       int x = lane / a.G;
       if (a.parents) {
@@ -329,25 +326,19 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
         } while (x >= 0);
         if (x != -1) m = 0;  // pruned: sees nothing
       } else {
-        m = x >= 31 ? 0xffffffffu : (2u << x) - 1;
+        m = (2u << x) - 1;
       }
-      aux.anc[warp][lane].x = m;
+      aux.anc[warp][lane] = m;
     }
     __syncwarp();
 
-    float o[MT][D / 8][4], m_ref[MT][2], l[MT][2];
+    float o[D / 8][4], m_ref[2], l[2];
+    m_ref[0] = m_ref[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m_ref[mt][h] = -INFINITY;
-        l[mt][h] = 0.f;
-      }
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[mt][d][x] = 0.f;
-    }
+      for (int x = 0; x < 4; ++x) o[d][x] = 0.f;
     bool any_bad = false;
 
 #pragma unroll 1
@@ -362,44 +353,37 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       if (!ok) break;
       const uint32_t kb_u = ring_u + slot * C::SLICE, vb_u = kb_u + C::KB * C::BLK;
 
-      float sc[MT][2][4];
+      float sc[2][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][t][x] = 0.f;
+        for (int x = 0; x < 4; ++x) sc[t][x] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t b[4];
         ldsm4(kb_u + (kk >> 2) * C::BLK + kr * 128 + (((2 * (kk & 3) + kc) ^ (kr & 7)) << 4), b);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16(sc[mt][0], qf[mt][kk], b[0], b[1]);
-          mma16(sc[mt][1], qf[mt][kk], b[2], b[3]);
-        }
+        mma16(sc[0], qf[kk], b[0], b[1]);
+        mma16(sc[1], qf[kk], b[2], b[3]);
       }
       if (!all) {
         const int off = s.L - key0;  // column of the first drafted key
         const uint32_t in = n_rows >= 16 ? 0xffffu : (1u << n_rows) - 1;  // n_rows >= 1
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t vis = in;
-            if (!mem) {
-              const uint32_t anc = aux.anc[warp][(mt * 16 + r4 + 8 * h)].x;
-              vis &= off >= 16   ? 0xffffu
-                     : off >= 0  ? (((1u << off) - 1) | (anc << off))
-                     : off > -32 ? anc >> -off
-                                 : 0u;
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-                if (!((vis >> (8 * t + c2 + x)) & 1)) sc[mt][t][2 * h + x] = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t vis = in;
+          if (!mem) {
+            const uint32_t anc = aux.anc[warp][r4 + 8 * h];
+            vis &= off >= 16   ? 0xffffu
+                   : off >= 0  ? (((1u << off) - 1) | (anc << off))
+                   : off > -32 ? anc >> -off
+                               : 0u;
           }
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (!((vis >> (8 * t + c2 + x)) & 1)) sc[t][2 * h + x] = -INFINITY;
+        }
         // clean V: rows past the end, non-finite drafted values
         unsigned char* v = ring + slot * C::SLICE + C::KB * C::BLK;
         bool bad = false;
@@ -423,57 +407,50 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
         tc::fence_proxy_async_smem();  // before the slot's next load
         __syncwarp();
       }
-      uint32_t pf[MT][4];
+      float mx[2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float mx[2];
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]),
+                      fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        mx[h] *= a.qscale;
+      }
+      // the reference maximum moves only when a slice exceeds it by 2^8
+      const bool g0 = mx[0] > m_ref[0] + kRescaleLog2, g1 = mx[1] > m_ref[1] + kRescaleLog2;
+      if (__any_sync(0xffffffffu, g0 || g1)) {
+        const float al0 = !g0 ? 1.f : m_ref[0] == -INFINITY ? 0.f : ex2a(m_ref[0] - mx[0]);
+        const float al1 = !g1 ? 1.f : m_ref[1] == -INFINITY ? 0.f : ex2a(m_ref[1] - mx[1]);
+        if (g0) m_ref[0] = mx[0];
+        if (g1) m_ref[1] = mx[1];
+        l[0] *= al0;
+        l[1] *= al1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
-                        fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-          mx[h] *= a.qscale;
+        for (int d = 0; d < D / 8; ++d) {
+          o[d][0] *= al0;
+          o[d][1] *= al0;
+          o[d][2] *= al1;
+          o[d][3] *= al1;
         }
-        // the reference maximum moves only when a slice exceeds it by 2^8
-        const bool g0 = mx[0] > m_ref[mt][0] + kRescaleLog2;
-        const bool g1 = mx[1] > m_ref[mt][1] + kRescaleLog2;
-        if (__any_sync(0xffffffffu, g0 || g1)) {
-          const float al0 = !g0 ? 1.f : m_ref[mt][0] == -INFINITY ? 0.f : ex2a(m_ref[mt][0] - mx[0]);
-          const float al1 = !g1 ? 1.f : m_ref[mt][1] == -INFINITY ? 0.f : ex2a(m_ref[mt][1] - mx[1]);
-          if (g0) m_ref[mt][0] = mx[0];
-          if (g1) m_ref[mt][1] = mx[1];
-          l[mt][0] *= al0;
-          l[mt][1] *= al1;
+      }
+      uint32_t pf[4];
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[mt][d][0] *= al0;
-            o[mt][d][1] *= al0;
-            o[mt][d][2] *= al1;
-            o[mt][d][3] *= al1;
-          }
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float nm = m_ref[h] == -INFINITY ? 0.f : -m_ref[h];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float nm = m_ref[mt][h] == -INFINITY ? 0.f : -m_ref[mt][h];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float p0 = ex2a(fmaf(sc[mt][t][2 * h], a.qscale, nm));
-            const float p1 = ex2a(fmaf(sc[mt][t][2 * h + 1], a.qscale, nm));
-            l[mt][h] += p0 + p1;
-            pf[mt][2 * t + h] = pack2(p0, p1);
-          }
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2a(fmaf(sc[t][2 * h], a.qscale, nm));
+          const float p1 = ex2a(fmaf(sc[t][2 * h + 1], a.qscale, nm));
+          l[h] += p0 + p1;
+          pf[2 * t + h] = pack2(p0, p1);
         }
       }
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         uint32_t b[4];
         ldsm4t(vb_u + (d >> 2) * C::BLK + vr * 128 + (((2 * (d & 3) + vc) ^ (vr & 7)) << 4), b);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16(o[mt][2 * d], pf[mt], b[0], b[1]);
-          mma16(o[mt][2 * d + 1], pf[mt], b[2], b[3]);
-        }
+        mma16(o[2 * d], pf, b[0], b[1]);
+        mma16(o[2 * d + 1], pf, b[2], b[3]);
       }
       __syncwarp();  // every lane has read the slot
       issue(slot);
@@ -487,55 +464,52 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     // write the item's share
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int h = 0; h < 2; ++h) {
+      const int r = r4 + 8 * h;
+      float lr = l[h];
+      lr += __shfl_xor_sync(0xffffffffu, lr, 1);
+      lr += __shfl_xor_sync(0xffffffffu, lr, 2);
+      if (r >= rows) continue;
+      const uint32_t anc = aux.anc[warp][r];
+      if (anc == 0) lr = 0.f;  // pruned
+      const int64_t prow = (worker * 2 + max(part, 0)) * part_rows + r;
+      const float inv = lr == 0.f ? 0.f : part >= 0 ? 1.f : 1.f / lr;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = mt * 16 + r4 + 8 * h;
-        float lr = l[mt][h];
-        lr += __shfl_xor_sync(0xffffffffu, lr, 1);
-        lr += __shfl_xor_sync(0xffffffffu, lr, 2);
-        if (r >= rows) continue;
-        if (aux.anc[warp][r].x == 0) lr = 0.f;  // pruned
-        const int64_t prow = (worker * 2 + max(part, 0)) * part_rows + r;
-        const float inv = part >= 0 ? (lr == 0.f ? 0.f : 1.f) : (lr == 0.f ? 0.f : 1.f / lr);
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          // (a row without weight: its O may hold 0 times NaN)
-          const float x = inv == 0.f ? 0.f : o[mt][d][2 * h] * inv;
-          const float y = inv == 0.f ? 0.f : o[mt][d][2 * h + 1] * inv;
-          if (part < 0)
-            *reinterpret_cast<uint32_t*>(out + out_row[mt][h] * D + d * 8 + c2) = pack2(x, y);
-          else
-            *reinterpret_cast<float2*>(part_o + prow * D + d * 8 + c2) = make_float2(x, y);
-        }
-        if (part >= 0 && c2 == 0) part_ml[prow] = make_float2(m_ref[mt][h], lr);
-        if (any_bad) {
-          // drafted values taken out of V, added for the rows that see them
-          const uint32_t anc = aux.anc[warp][r].x;
+      for (int d = 0; d < D / 8; ++d) {
+        // (a row without weight: its O may hold 0 times NaN)
+        const float x = inv == 0.f ? 0.f : o[d][2 * h] * inv;
+        const float y = inv == 0.f ? 0.f : o[d][2 * h + 1] * inv;
+        if (part < 0)
+          *reinterpret_cast<uint32_t*>(out + out_row[h] * D + d * 8 + c2) = pack2(x, y);
+        else
+          *reinterpret_cast<float2*>(part_o + prow * D + d * 8 + c2) = make_float2(x, y);
+      }
+      if (part >= 0 && c2 == 0) part_ml[prow] = make_float2(m_ref[h], lr);
+      if (!any_bad) continue;
+      // drafted values taken out of V, added for the rows that see them
 #pragma unroll 1
-          for (int t = 0; t < s.n; ++t) {
-            const int kr2 = s.L + t, j = n_ms + kr2 / kSlice;
-            if (!((anc >> t) & 1) || j < j_lo || j >= j_lo + cnt || kr2 >= s.cache) continue;
-            const int pg = a.block_table[(int64_t)cu.b * a.max_pages + kr2 / a.page_size];
-            if (pg < 0 || pg >= a.n_pages) continue;
-            const __nv_bfloat16* v =
-                static_cast<const __nv_bfloat16*>(a.v_pages) +
-                (((int64_t)pg * a.H + cu.g) * a.page_size + kr2 % a.page_size) * D;
+      for (int t = 0; t < s.n; ++t) {
+        const int kr2 = s.L + t, j = n_ms + kr2 / kSlice;
+        if (!((anc >> t) & 1) || j < j_lo || j >= j_lo + cnt || kr2 >= s.cache) continue;
+        const int pg = a.block_table[(int64_t)cu.b * a.max_pages + kr2 / a.page_size];
+        if (pg < 0 || pg >= a.n_pages) continue;
+        const __nv_bfloat16* v =
+            static_cast<const __nv_bfloat16*>(a.v_pages) +
+            (((int64_t)pg * a.H + cu.g) * a.page_size + kr2 % a.page_size) * D;
 #pragma unroll 1
-            for (int d = 0; d < D / 4; ++d) {  // this thread's columns
-              const int col = 8 * (d >> 1) + c2 + (d & 1);
-              const float f = __bfloat162float(v[col]);
-              if (isfinite(f)) continue;
-              if (part < 0) {
-                __nv_bfloat16* p = out + out_row[mt][h] * D + col;
-                *p = __float2bfloat16(__bfloat162float(*p) + f);
-              } else {
-                part_o[prow * D + col] += f;
-              }
-            }
+        for (int d = 0; d < D / 4; ++d) {  // this thread's columns
+          const int col = 8 * (d >> 1) + c2 + (d & 1);
+          const float f = __bfloat162float(v[col]);
+          if (isfinite(f)) continue;
+          if (part < 0) {
+            __nv_bfloat16* p = out + out_row[h] * D + col;
+            *p = __float2bfloat16(__bfloat162float(*p) + f);
+          } else {
+            part_o[prow * D + col] += f;
           }
         }
       }
+    }
     cu.left -= cnt;
     cu.j += cnt;
     if (cu.left > 0) cu.next_item(a.H, seq);
@@ -567,9 +541,9 @@ FewPlan few_plan(int n_max, int G, int D) {
   return p;
 }
 
-template <int D, int MT>
+template <int D>
 int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
-  using C = FC<D, MT>;
+  using C = FC<D>;
   const FewPlan p = few_plan(a.n_max, a.G, D);
   unsigned char* w = static_cast<unsigned char*>(ws);
   float* part_o = reinterpret_cast<float*>(w);
@@ -585,7 +559,7 @@ int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
   else
     km = kp, vm = vp;  // never loaded from
   if (!ok) return note_cuda(cudaErrorInvalidValue);
-  auto kern = tree_few_kernel<D, MT>;
+  auto kern = tree_few_kernel<D>;
   if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)C::SMEM)) return rc;
   const unsigned grid = (unsigned)num_sms();
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kFewThreads), C::SMEM, s, km, vm, kp, vp, a,
@@ -596,13 +570,15 @@ int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
 
 }  // namespace
 
-bool tree_few_takes(int n_max, int G) { return n_max * G <= 32; }
+// One row tile of the warp's instructions.  (With two, 17 to 32 rows, a slice
+// took a warp so long that loads waited: 16 sequences x 8,220 keys, 32 rows,
+// 125 us against tree_attn_tc.cu's 103 for 36; 64 sequences x 100 keys 46 us
+// against 24.)
+bool tree_few_takes(int n_max, int G) { return n_max * G <= 16; }
 size_t tree_few_workspace_size(int n_max, int G, int D) { return few_plan(n_max, G, D).total; }
 
 int tree_few_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s) {
-  const bool two = a.n_max * a.G > 16;
-  if (D == 64) return two ? launch_few<64, 2>(a, ws, s) : launch_few<64, 1>(a, ws, s);
-  return two ? launch_few<128, 2>(a, ws, s) : launch_few<128, 1>(a, ws, s);
+  return D == 64 ? launch_few<64>(a, ws, s) : launch_few<128>(a, ws, s);
 }
 
 }  // namespace msa
