@@ -52,16 +52,17 @@ namespace {
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kMemRows = 32;    // memory rows of one load
 constexpr int kTcThreads = 384; // 4 single warps, 2 softmax warpgroups
-constexpr int kMaxSt = 6;       // K or V ring slots at most
+constexpr int kRing = 64 * 1024; // the K ring, and the V ring
+constexpr int kStage = 4096;    // an output buffer of each softmax warp
 constexpr int kSched = 3;       // published items
 constexpr int kReaders = 11;    // K warp, V warp, MMA, 8 softmax warps
 constexpr int kItemCost = 3;    // what an item's start and end cost, in tiles
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kSmemMax = 227 * 1024;
 
 template <int D> struct TC {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kKeys * 128;  // a K or V tile
+  static constexpr int ST = kRing / TILE;        // ring slots
   static constexpr uint32_t IDESC_S = tc::idesc_bf16_f32(128, kKeys);
   static constexpr uint32_t IDESC_O = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V MN-major
   // registers: 128 x LOW + 256 x HIGH = 384 x 168, the launch's allocation
@@ -79,7 +80,7 @@ struct ItemE {
 };
 
 struct Aux {
-  uint64_t kfull[kMaxSt], kfree[kMaxSt], vfull[kMaxSt], vfree[kMaxSt];
+  uint64_t kfull[4], kfree[4], vfull[4], vfree[4];  // ring slots, 4 at most
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_empty[2], ml_full;
   uint64_t sched_full[kSched], par_full[kSched], sched_empty[kSched];
   ItemE item[kSched];
@@ -92,8 +93,9 @@ struct Aux {
   uint32_t tmem_base;
   int abort_flag;
 };
-// two Q buffers of 128 rows and five ring slots of 32 KB leave it this much
-static_assert(sizeof(Aux) <= 2048, "shared memory");
+// two Q buffers of 128 rows, the rings and the output buffers leave it this much
+static_assert(1024 + 2 * 128 * 256 + 2 * kRing + 8 * kStage + sizeof(Aux) <= 227 * 1024,
+              "shared memory");
 
 __device__ __forceinline__ float ex2a(float x) {
   float y;
@@ -143,7 +145,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ CUtensorMap tm_km, const __grid_constant__ CUtensorMap tm_vm,
                const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                const __grid_constant__ TreeArgs a, int part_rows, int tile_rows,
-               int q_rows, int n_k, int n_v, float* __restrict__ part_o, float2* __restrict__ part_ml,
+               int q_rows, float* __restrict__ part_o, float2* __restrict__ part_ml,
                TreeCut* __restrict__ cuts) {
   using C = TC<D>;
   constexpr int KB = C::KB;
@@ -156,13 +158,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int q_tile = KB * q_rows * 128;
   unsigned char* sQ = base;
   unsigned char* sK = sQ + 2 * q_tile;
-  unsigned char* sV = sK + n_k * C::TILE;
-  Aux& aux = *reinterpret_cast<Aux*>(sV + n_v * C::TILE);
+  unsigned char* sV = sK + kRing;
+  unsigned char* sOut = sV + kRing;
+  Aux& aux = *reinterpret_cast<Aux*>(sOut + 8 * kStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < kMaxSt; ++i) {
+    for (int i = 0; i < C::ST; ++i) {
       tc::mbar_init(&aux.kfull[i], 1);
       tc::mbar_init(&aux.kfree[i], 1);
       tc::mbar_init(&aux.vfull[i], 1);
@@ -374,7 +377,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       unsigned char* ring = isv ? sV : sK;
       uint64_t* full = isv ? aux.vfull : aux.kfull;
       uint64_t* fre = isv ? aux.vfree : aux.kfree;
-      const int n_st = isv ? n_v : n_k;
+      const int n_st = C::ST;
       const CUtensorMap* mm = isv ? &tm_vm : &tm_km;
       const CUtensorMap* mp = isv ? &tm_vp : &tm_kp;
       const int page = a.page_size;
@@ -473,7 +476,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       uint32_t kph = 0, vph = 0;
       auto next_k = [&]() {
         tc::mma_commit(&aux.kfree[kst]);
-        if (++kst == n_k) {
+        if (++kst == C::ST) {
           kst = 0;
           kph ^= 1;
         }
@@ -512,7 +515,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (j + 2 == cnt) tc::mma_commit(&aux.q_free[0]);
           }
           tc::mma_commit(&aux.vfree[vst]);
-          if (++vst == n_v) {
+          if (++vst == C::ST) {
             vst = 0;
             vph ^= 1;
           }
@@ -550,7 +553,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             issue_pv(s, vst, first ? 0u : 1u);
             if (i_p + 2 >= n_p) tc::mma_commit(&aux.o_full[s]);
             tc::mma_commit(&aux.vfree[vst]);
-            if (++vst == n_v) {
+            if (++vst == C::ST) {
               vst = 0;
               vph ^= 1;
             }
@@ -575,7 +578,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (q_seen && tc::mbar_test(&aux.kfull[kst], kph)) {
               issue_s(s, qb, kst);
               tc::mma_commit(&aux.kfree[kst]);
-              if (++kst == n_k) {
+              if (++kst == C::ST) {
                 kst = 0;
                 kph ^= 1;
               }
@@ -664,23 +667,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             // tile, so the parity names this tile; P V waits for this
             // group's p_full below
             const uint32_t vi = u + i;
-            if (!wait(&aux.vfull[vi % n_v], (vi / n_v) & 1)) break;
-            unsigned char* vr = sV + (vi % n_v) * C::TILE + r * 128;
+            if (!wait(&aux.vfull[vi % C::ST], (vi / C::ST) & 1)) break;
+            // rows to look at: past the end, and drafted ones another row may
+            // not see; 16-byte pieces, consecutive ones by consecutive threads
+            unsigned char* vt = sV + (vi % C::ST) * C::TILE;
+            const int first = mem || e.n == 1 ? n_rows : max(min(n_rows, e.L - key0), 0);
             bool bad = false;
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * (kKeys * 128) + ((c & 7) << 4));
-              if (r >= n_rows) {
-                *p = make_uint4(0, 0, 0, 0);
-              } else if (!mem && key0 + r >= e.L) {
-                const uint4 x = *p;
-                const uint4 y = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y),
-                                           finite_bf16x2(x.z), finite_bf16x2(x.w));
-                if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-                  *p = y;
-                  bad = true;
-                }
+#pragma unroll 4
+            for (int p = first * (D / 8) + r; p < kKeys * (D / 8); p += 128) {
+              const int vrow = p / (D / 8), c = p % (D / 8);
+              uint4* v =
+                  reinterpret_cast<uint4*>(vt + (c >> 3) * (kKeys * 128) + vrow * 128 + (c & 7) * 16);
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (vrow < n_rows) {
+                const uint4 y = *v;
+                x = make_uint4(finite_bf16x2(y.x), finite_bf16x2(y.y), finite_bf16x2(y.z),
+                               finite_bf16x2(y.w));
+                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+                bad = true;
               }
+              *v = x;
             }
             if (bad) *(volatile int*)&aux.bad[k % kSched] = (int)k + 1;
             tc::fence_proxy_async_smem();
@@ -804,7 +810,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             c1 *= inv;
           }
           // (a small loop: this code runs once an item, and what it costs first
-          // is its way into the instruction cache)
+          // is its way into the instruction cache; and by way of shared memory:
+          // a thread holds a row, and a warp's stores of 16 bytes of each of 32
+          // rows took an item of 256 rows 13,000 cycles)
           const int64_t prow = ((int64_t)blockIdx.x * 2 + e.part) * part_rows + rb;
           if (warp_on) {
             const uint32_t tO = tmem + 256 + grp * D + lane_addr;
@@ -812,32 +820,59 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) +
                                 ((e.t0 + tok) * a.Hq + e.g * G + row % G) * D;
             float* po = part_o + prow * D;
+            const uint64_t mine = e.part < 0 ? reinterpret_cast<uint64_t>(op)
+                                             : reinterpret_cast<uint64_t>(po);
+            const uint32_t live = __ballot_sync(0xffffffffu, row_ok);
+            unsigned char* stg = sOut + (warp - 4) * kStage;  // 32 rows of 128 bytes
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t x0[16], x1[16];
               float o[16];
               tc::tmem_ld16(tO + c, x0);
-              tc::tmem_ld16(tO2 + c, x1);
+              if (kQT == 1) tc::tmem_ld16(tO2 + c, x1);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x)
-                o[x] = (c0 == 0.f ? 0.f : c0 * __uint_as_float(x0[x])) +
-                       (c1 == 0.f ? 0.f : c1 * __uint_as_float(x1[x]));
-              if (row_ok) {
-                if (e.part < 0) {
-#pragma unroll
-                  for (int x = 0; x < 16; x += 8)
-                    st16(op + c + x,
-                         make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]),
-                                    pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7])));
-                } else {
-#pragma unroll
-                  for (int x = 0; x < 16; x += 4)
-                    *reinterpret_cast<float4*>(po + c + x) =
-                        make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                }
+              for (int x = 0; x < 16; ++x) {
+                o[x] = c0 == 0.f ? 0.f : c0 * __uint_as_float(x0[x]);
+                if (kQT == 1) o[x] += c1 == 0.f ? 0.f : c1 * __uint_as_float(x1[x]);
               }
-              __syncwarp();  // the next load is the whole warp's
+              // 16-byte pieces of a row: columns c .. of 64 bf16, or of 32 fp32
+              int p0;
+              auto put = [&](int p, const uint4& v) {
+                *reinterpret_cast<uint4*>(stg + lane * 128 + ((p ^ (lane & 7)) << 4)) = v;
+              };
+              if (e.part < 0) {
+                p0 = (c & 63) >> 3;
+#pragma unroll
+                for (int x = 0; x < 16; x += 8)
+                  put(p0 + (x >> 3),
+                      make_uint4(pack2(o[x], o[x + 1]), pack2(o[x + 2], o[x + 3]),
+                                 pack2(o[x + 4], o[x + 5]), pack2(o[x + 6], o[x + 7])));
+                p0 += 2;
+              } else {
+                p0 = (c & 31) >> 2;
+#pragma unroll
+                for (int x = 0; x < 16; x += 4)
+                  put(p0 + (x >> 2),
+                      make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
+                                 __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+                p0 += 4;
+              }
+              __syncwarp();
+              if (p0 == 8) {  // eight lanes a row, four rows a store
+                const uint64_t at =
+                    (uint64_t)(e.part < 0 ? (c & ~63) * 2 : (c & ~31) * 4) + (lane & 7) * 16;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const int rw = x * 4 + (lane >> 3);
+                  const uint64_t dst = __shfl_sync(0xffffffffu, mine, rw) + at;
+                  if ((live >> rw) & 1)
+                    st16(reinterpret_cast<void*>(dst),
+                         *reinterpret_cast<const uint4*>(stg + rw * 128 +
+                                                         (((lane & 7) ^ (rw & 7)) << 4)));
+                }
+                __syncwarp();
+              }
             }
             if (row_ok && e.part >= 0) part_ml[prow] = make_float2(m_run, l_run);
             if (row_ok && bad) {
@@ -895,14 +930,13 @@ struct TcPlan {
   int qt;          // Q tiles of an item
   int part_rows;   // rows of a partial
   int tile_tok;    // tokens of a tile: whole tokens, at most 128 rows
-  int q_rows, n_k, n_v;
+  int q_rows;
   size_t smem, po_bytes, ml_bytes, cut_bytes, total;
 };
 
 // kQT = 2 once an item's rows exceed one MMA tile: both tiles then share one
-// pass over K and V.  The Q buffers hold no more rows than a tile can have
-// (the MMA reads on into the ring: rows of S that nobody reads), what
-// they leave goes to the rings.
+// pass over K and V.  The Q buffers hold no more rows than a tile can have (the
+// MMA reads on into the ring: rows of S that nobody reads).
 TcPlan tc_plan(int n_max, int G, int D) {
   TcPlan p{};
   const int rows = n_max * G;
@@ -910,12 +944,7 @@ TcPlan tc_plan(int n_max, int G, int D) {
   p.tile_tok = std::min(n_max, 128 / G);
   p.part_rows = std::min(rows, p.tile_tok * G * p.qt);
   p.q_rows = (p.tile_tok * G + 7) / 8 * 8;
-  const int tile = D / 64 * kKeys * 128;
-  const int q_bytes = 2 * (D / 64) * p.q_rows * 128;
-  const int slots = (kSmemMax - 1024 - (int)sizeof(Aux) - q_bytes) / tile;
-  p.n_v = std::min(kMaxSt, (slots + 1) / 2);
-  p.n_k = std::min(kMaxSt, slots - p.n_v);
-  p.smem = 1024 + q_bytes + (size_t)(p.n_k + p.n_v) * tile + sizeof(Aux);
+  p.smem = 1024 + 2 * (size_t)(D / 64) * p.q_rows * 128 + 2 * kRing + 8 * kStage + sizeof(Aux);
   const size_t parts = 2 * (size_t)num_sms() * p.part_rows;
   p.po_bytes = round_up(parts * D * sizeof(float), 256);
   p.ml_bytes = round_up(parts * sizeof(float2), 256);
@@ -945,7 +974,7 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)p.smem)) return rc;
   const unsigned grid = (unsigned)num_sms();
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, qm, km, vm, kp, vp, a,
-                          p.part_rows, p.tile_tok * a.G, p.q_rows, p.n_k, p.n_v, part_o, part_ml, cuts))
+                          p.part_rows, p.tile_tok * a.G, p.q_rows, part_o, part_ml, cuts))
     return rc;
   return tree_merge_launch(a, D, (int)grid, 1, p.part_rows, part_o, part_ml, cuts, s);
 }
