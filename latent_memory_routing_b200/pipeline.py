@@ -447,7 +447,9 @@ class PagedCache:
 
 class TreeAttention:
     """Holds the workspace of msa_tree_attn for fixed shapes: up to ``n_max``
-    drafted tokens a sequence over [memory ; paged cache ; drafted tokens]."""
+    drafted tokens a sequence over [memory ; paged cache ; drafted tokens].
+    Calls of one object use one workspace: they run one after another (one
+    stream, or graphs that do not replay at the same time)."""
 
     def __init__(self, dtype, B, n_max, Hq, H, D, m_cap, max_pages, page_size, device):
         self.dt = _m.dtype_code(dtype)

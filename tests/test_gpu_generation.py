@@ -436,6 +436,38 @@ def test_tree_attention(case):
     status()
 
 
+@pytest.mark.parametrize("dt,Hq,n", [(F32, 2, 2), (BF16, 2, 2), (BF16, 1, 18), (BF16, 8, 17)],
+                         ids=["f32", "bf16", "bf16-18rows", "bf16-136rows"])
+def test_many_short_sequences(dt, Hq, n):
+    """More sequences than a CTA has threads, many of them without tokens."""
+    B = 700
+    r = np.random.default_rng(5)
+    toks = [int(x) for x in r.integers(0, n + 1, B)]
+    lens = [int(x) for x in r.integers(0, 40, B)]
+    toks[17], lens[17] = n, 200
+    t = tree_case(dt, 16, Hq, 1, 64, lens, toks, [], "chain", seed=1)
+    check_tree(t, run_tree(t, n))
+    status()
+
+
+@pytest.mark.parametrize("n_max", [1, 4, 5, 8, 9, 32, 33, 100, 128])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_row_counts_around_the_kernels_tiles(dt, n_max):
+    """Four heads a group: 4 to 512 rows, in full and in part."""
+    t = tree_case(dt, 32, 4, 1, 128, [190, 7, 0], [n_max, 1, max(1, n_max // 2)], [33, 1, 0],
+                  "tree", seed=n_max)
+    check_tree(t, run_tree(t, n_max))
+    status()
+
+
+def test_few_tokens_where_many_were_allowed():
+    """n_max bounds the work; the tokens may be fewer."""
+    t = tree_case(BF16, 64, 8, 2, 128, [500, 70], [2, 1], [9, 0], "tree", seed=3)
+    for n_max in (2, 20, 128):
+        check_tree(t, run_tree(t, n_max))
+    status()
+
+
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_padding_tokens_are_left_alone_and_scale_is_used(dt):
     t = tree_case(dt, 32, 8, 4, 64, [40, 3], [5, 9], [10, 2], "tree", seed=2, lead=4)
@@ -443,7 +475,8 @@ def test_padding_tokens_are_left_alone_and_scale_is_used(dt):
     status()
 
 
-@pytest.mark.parametrize("dt,D,n", [(F32, 64, 20), (BF16, 64, 20), (BF16, 128, 100)])
+@pytest.mark.parametrize("dt,D,n", [(F32, 64, 12), (F32, 64, 20), (BF16, 64, 8), (BF16, 64, 20),
+                                    (BF16, 128, 100)])
 def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n):
     """A drafted token's NaN or infinite K and V reach the rows that see it
     and no others."""
@@ -751,3 +784,66 @@ def test_a_backward_call_on_another_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for g in got for a, b in zip(want, g))
     status()
+
+
+DEBUG_CHILD = r"""
+import torch
+from latent_memory_routing_b200 import msa, pipeline
+
+assert msa.LIB_PATH.endswith("libmsa_debug.so"), msa.LIB_PATH
+msa.lib()
+msa.msa_device_status(clear=True)
+
+def refused(fn, code):
+    try:
+        fn()
+    except msa.MsaError as e:
+        assert e.status == code, (e.status, code)
+        msa.msa_device_status(clear=True)
+        return
+    raise AssertionError("the call was not refused")
+
+def i32(x): return torch.tensor(x, dtype=torch.int32, device="cuda")
+def i64(x): return torch.tensor(x, dtype=torch.int64, device="cuda")
+
+for dt in (torch.float32, torch.bfloat16):
+    c = pipeline.PagedCache(dt, 8, 16, 2, 64, 2, 3, "cuda")
+    for b in range(2):
+        c.reserve(b, 40)
+    k, q = torch.randn(6, 2, 64, device="cuda").to(dt), torch.randn(6, 4, 64, device="cuda").to(dt)
+    off, pos = i64([0, 4, 6]), i32([0, 1, 2, 3, 0, 1])
+    att = pipeline.TreeAttention(dt, 2, 4, 4, 2, 64, 0, 3, 16, "cuda")
+    c.append(k, k, off, pos)
+    out = att(q, off, c)
+    assert bool(torch.isfinite(out).all())
+    refused(lambda: c.append(k, k, i64([0, 5, 4]), pos), -1)    # offsets that fall
+    refused(lambda: att(q, i64([0, 5, 4]), c), -1)
+    refused(lambda: att(q, off, c, parents=i32([0, 0, 0, 0, -1, 0])), -1)  # its own parent
+    c.cache_len[1] = 49                                         # past the block table
+    refused(lambda: c.append(k, k, off, pos), -1)
+    refused(lambda: att(q, off, c), -1)
+    c.cache_len[1] = 47                                         # its second row has no place
+    refused(lambda: c.append(k, k, off, pos), -3)
+    c.cache_len[1] = 0
+    assert torch.equal(att(q, off, c), out)
+    y = pipeline.qk_norm_rope(q, k, pos)
+    dy = [x.float() for x in y]
+    pipeline.qk_norm_rope_backward(q, k, pos, *dy)
+    assert msa.msa_device_status(clear=True) == 0
+print("debug build ok")
+"""
+
+
+def test_debug_library_refuses_bad_arrays(cuda_device):
+    """The input-checking build returns what its calls find from the calls."""
+    import os
+    import subprocess
+    import sys
+
+    from latent_memory_routing_b200 import build
+    build.build(debug=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD], cwd=root, capture_output=True, text=True,
+                       env=dict(os.environ, MSA_DEBUG="1"), timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
+    assert "debug build ok" in r.stdout
