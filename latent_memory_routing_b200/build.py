@@ -5,7 +5,8 @@
 Each csrc/*.cu is compiled to an object in parallel (nvcc -c), then linked
 into latent_memory_routing_b200/libmsa.so with the static CUDA runtime (no
 -lcuda: the driver's tensor-map encoder is resolved at run time).  Objects
-are rebuilt only when a source or header is newer.
+are rebuilt only when a source or header is newer.  csrc/marshal.cpp, a CPython
+extension of the ctypes binding, is built beside it with g++.
 
 ``--debug`` builds libmsa_debug.so instead, from the same sources with
 -DMSA_DEBUG: every entry point validates the device-side index arrays it is
@@ -23,12 +24,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(os.path.dirname(PKG), "_build")
 LIB = os.path.join(PKG, "libmsa.so")
 LIB_DEBUG = os.path.join(PKG, "libmsa_debug.so")
+MARSHAL = os.path.join(PKG, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
          "--expt-relaxed-constexpr", "-DNDEBUG"]
@@ -71,6 +74,27 @@ def _uses_debug_hooks(src: str) -> bool:
     return "debug_check_" in text or "debug_finish" in text or "MSA_DEBUG" in text
 
 
+def build_marshal() -> str | None:
+    """The native argument marshalling (csrc/marshal.cpp) for this
+    interpreter; None where there is no C++ compiler or no Python headers (the
+    binding then does the same in Python)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    include = sysconfig.get_paths()["include"]
+    cxx = shutil.which("g++")
+    if cxx is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    if (os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src)
+            and os.path.getmtime(MARSHAL) >= _newest_header()):
+        return MARSHAL
+    tmp = MARSHAL + ".tmp"
+    r = subprocess.run([cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                        "-I", include, "-o", tmp, src], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
     debug_dir = os.path.join(BUILD, "debug")
@@ -78,6 +102,7 @@ def build(verbose: bool = False, debug: bool = False) -> str:
     if debug:
         os.makedirs(debug_dir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    build_marshal()
 
     def obj(src: str) -> str:
         if debug and _uses_debug_hooks(src):

@@ -525,10 +525,49 @@ def msa_encode_pool_backward(L, n_tok, n_docs, H, D, dk_bar, dv_bar, dkr_bar, to
         _stream(stream)))
 
 
+# The native marshalling of the calls below (csrc/marshal.cpp): it does what
+# the Python path of each does where every check passes, and returns None,
+# without having called the library, where one does not.
+_bound: list = [None, None]  # the library handle it was bound to, the module
+
+
+def _native():
+    handle = lib()
+    if handle is not _bound[0]:
+        module = None
+        if isinstance(handle, ctypes.CDLL):
+            try:
+                from . import _marshal as module
+            except ImportError:  # not built: the Python path alone
+                module = None
+        if module is not None:
+            torch = _th()
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            dev = getattr(torch._C, "_cuda_getDevice", None)
+            if raw is None or dev is None:
+                module = None
+            else:
+                module.bind(
+                    tuple(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value for name in
+                          ("msa_qk_norm_rope", "msa_qk_norm_rope_backward", "msa_paged_append",
+                           "msa_tree_attn")),
+                    (torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8), dev,
+                    raw)
+        _bound[:] = [handle, module]
+    return _bound[1]
+
+
 def msa_qk_norm_rope(dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base,
                      q_out, k_out, stream=None):
     """q and k: [n_tok][heads][D] tensors, the token strides taken from them
     (raw addresses are dense)."""
+    native = _native()
+    if native is not None:
+        rc = native.msa_qk_norm_rope(
+            dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base, q_out, k_out,
+            stream)
+        if rc is not None:
+            return _check("msa_qk_norm_rope", rc)
     es, dev = _es(dt), _device()
     qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
     kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
@@ -548,6 +587,13 @@ def msa_qk_norm_rope_backward(dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_we
                               ws_bytes, stream=None):
     """q, k, dq and dk: [n_tok][heads][D] tensors, the token strides taken
     from them (raw addresses are dense)."""
+    native = _native()
+    if native is not None:
+        rc = native.msa_qk_norm_rope_backward(
+            dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base, dq_out,
+            dk_out, dq, dk, dq_weight, dk_weight, ws, ws_bytes, stream)
+        if rc is not None:
+            return _check("msa_qk_norm_rope_backward", rc)
     es, gs, dev = _es(dt), _es(grad_dt), _device()
     qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
     kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
@@ -569,6 +615,14 @@ def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_of
                      k_pages, v_pages, q_out, stream=None):
     """q, k and v: [n_tok][heads][D] tensors, the token strides taken from
     them (raw addresses are dense)."""
+    native = _native()
+    if native is not None:
+        rc = native.msa_paged_append(
+            dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_offsets, positions, eps,
+            rope_base, block_table, max_pages, cache_len, page_size, n_pages, k_pages, v_pages, q_out,
+            stream)
+        if rc is not None:
+            return _check("msa_paged_append", rc)
     es, dev = _es(dt), _device()
     qp, qs = _rows(q, n_tok, Hq, D, "q", es, dev)
     kp, ks = _rows(k, n_tok, H, D, "k", es, dev)
@@ -592,6 +646,14 @@ def msa_tree_attn_workspace_size(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_
 def msa_tree_attn(dt, B, n_tok, n_max, Hq, H, D, q, tok_offsets, parents, k_mem, v_mem, mem_len,
                   m_cap, k_pages, v_pages, n_pages, page_size, block_table, max_pages, cache_len,
                   scale, out, ws, ws_bytes, stream=None):
+    native = _native()
+    if native is not None:
+        rc = native.msa_tree_attn(
+            dt, B, n_tok, n_max, Hq, H, D, q, tok_offsets, parents, k_mem, v_mem, mem_len, m_cap,
+            k_pages, v_pages, n_pages, page_size, block_table, max_pages, cache_len, scale, out, ws,
+            ws_bytes, stream)
+        if rc is not None:
+            return _check("msa_tree_attn", rc)
     es, dev = _es(dt), _device()
     rows, mem, pool = n_tok * Hq * D, B * m_cap * H * D, n_pages * H * page_size * D
     _ws_ok(ws, ws_bytes)

@@ -378,7 +378,7 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     n, _, D = x.shape
 
     def grad(t, w):
-        return None if t is None or w is None else t.new_empty(D, dtype=torch.float32)
+        return None if t is None or w is None else torch.empty_like(w, dtype=torch.float32)
 
     if ws is None:
         ws = _made(stream, lambda: qk_norm_rope_backward_workspace(q, k))

@@ -19,6 +19,8 @@ rounded to bf16 moves by at most 2^-8 of itself.
   the sums over N keys by N U; bf16 weights move the output by 2^-8 A.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -783,6 +785,65 @@ def test_a_backward_call_on_another_stream():
     got = [pipeline.qk_norm_rope_backward(q, k, pos, dq, dk, wq, wk, stream=s) for _ in range(5)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for g in got for a, b in zip(want, g))
+    status()
+
+
+@pytest.fixture(params=["native", "python"])
+def marshalling(request):
+    """The calls' arguments checked by the native module, or in Python."""
+    native = msa._native()
+    assert native is not None
+    if request.param == "python":
+        msa._bound[1] = None
+    yield request.param
+    msa._bound[1] = native
+
+
+def test_binding_takes_what_fits_and_refuses_the_rest(marshalling):
+    dt, D = BF16, 64
+    _, (q, k, v) = fused(6, 4, 2, D, dt, 1)
+    w, pos, off = rnd((D,), dt, 2), i32(np.arange(6)), i64([0, 4, 6])
+    c = pipeline.PagedCache(dt, 8, 16, 2, D, 2, 3, "cuda")
+    for b in range(2):
+        c.reserve(b, 40)
+    qr = c.append(k, v, off, pos, w, q, w)
+    att = pipeline.TreeAttention(dt, 2, 4, 4, 2, D, 0, 3, 16, "cuda")
+    out = att(qr, off, c)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    again = [att(qr, off, c, stream=side), att(qr, off, c, stream=side.cuda_stream)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, out) for x in again)
+    dq, dk = (x.float() for x in pipeline.qk_norm_rope(q, k, pos, w, w))
+    pipeline.qk_norm_rope_backward(q, k, pos, dq, dk, w, w)
+    torch.cuda.synchronize()
+
+    def no(match, fn):
+        with pytest.raises(ValueError, match=match):
+            fn()
+
+    no("v is torch.float32", lambda: c.append(k, v.float(), off, pos))
+    no("tok_offsets is torch.int32", lambda: c.append(k, v, off.int(), pos))
+    no("positions holds 5", lambda: c.append(k, v, off, pos[:5]))
+    no("q must be contiguous", lambda: att(q, off, c))
+    no("heads must be contiguous", lambda: c.append(k.transpose(0, 1).contiguous().transpose(0, 1),
+                                                    v, off, pos))
+    no("v has shape", lambda: c.append(k, v[:, :1], off, pos))
+    no("parents is on cpu", lambda: att(qr, off, c, parents=torch.zeros(6, dtype=torch.int32)))
+    no("q_weight is on cpu", lambda: pipeline.qk_norm_rope(q, k, pos, w.cpu()))
+    no("dq_out is torch.float64", lambda: msa.msa_qk_norm_rope_backward(
+        1, 0, 6, 4, 0, D, q, None, None, None, pos, 1e-6, 1e4, dq.double(), None, dq, None, None,
+        None, None, 0))
+    no("ws holds", lambda: msa.msa_tree_attn(
+        1, 2, 6, 4, 4, 2, D, qr, off, None, None, None, None, 0, c.k_pages, c.v_pages, 8, 16,
+        c.block_table, 3, c.cache_len, 0.0, out, att.ws, att.ws.numel() + 1))
+    with pytest.raises(msa.MsaError) as e:
+        msa.msa_tree_attn(1, 2, 6, 4, 4, 2, D, qr, off, None, None, None, None, 0, c.k_pages,
+                          c.v_pages, 8, 16, c.block_table, 3, c.cache_len, 0.0, out, att.ws, 8)
+    assert e.value.status == -6
+    with pytest.raises(ctypes.ArgumentError):
+        pipeline.qk_norm_rope(q, k, pos, w, w, eps="small")
+    assert torch.equal(att(qr, off, c), out)
     status()
 
 
