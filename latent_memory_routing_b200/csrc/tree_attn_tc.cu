@@ -682,8 +682,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll 4
             for (int p = first * (D / 8) + r; p < kKeys * (D / 8); p += 128) {
               const int vrow = p / (D / 8), c = p % (D / 8);
-              uint4* v =
-                  reinterpret_cast<uint4*>(vt + (c >> 3) * (kKeys * 128) + vrow * 128 + (c & 7) * 16);
+              uint4* v = reinterpret_cast<uint4*>(vt + (c >> 3) * (kKeys * 128) + vrow * 128 +
+                                                  (c & 7) * 16);
               uint4 x = make_uint4(0, 0, 0, 0);
               if (vrow < n_rows) {
                 const uint4 y = *v;

@@ -590,8 +590,8 @@ def msa_qk_norm_rope_backward(dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_we
     native = _native()
     if native is not None:
         rc = native.msa_qk_norm_rope_backward(
-            dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base, dq_out,
-            dk_out, dq, dk, dq_weight, dk_weight, ws, ws_bytes, stream)
+            dt, grad_dt, n_tok, Hq, H, D, q, k, q_weight, k_weight, positions, eps, rope_base,
+            dq_out, dk_out, dq, dk, dq_weight, dk_weight, ws, ws_bytes, stream)
         if rc is not None:
             return _check("msa_qk_norm_rope_backward", rc)
     es, gs, dev = _es(dt), _es(grad_dt), _device()
@@ -619,8 +619,8 @@ def msa_paged_append(dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_of
     if native is not None:
         rc = native.msa_paged_append(
             dt, B, n_tok, Hq, H, D, q, k, v, q_weight, k_weight, tok_offsets, positions, eps,
-            rope_base, block_table, max_pages, cache_len, page_size, n_pages, k_pages, v_pages, q_out,
-            stream)
+            rope_base, block_table, max_pages, cache_len, page_size, n_pages, k_pages, v_pages,
+            q_out, stream)
         if rc is not None:
             return _check("msa_paged_append", rc)
     es, dev = _es(dt), _device()

@@ -337,6 +337,14 @@ def _heads(t):
     return 0 if t is None else t.shape[1]
 
 
+def _same_tokens(n, D, **tensors):
+    """Every tensor given is [n][heads][D]: rows of a longer one would be left
+    out of the call, and out of what it returns."""
+    for what, t in tensors.items():
+        if t is not None and (t.dim() != 3 or t.shape[0] != n or t.shape[2] != D):
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, needs [{n}, heads, {D}]")
+
+
 def _dense(t):
     """An uninitialised contiguous tensor like t (None for None)."""
     return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -350,11 +358,14 @@ def qk_norm_rope(q, k, positions=None, q_weight=None, k_weight=None, eps: float 
     of q and k may lie apart (slices of a fused projection's output); the
     outputs are contiguous.  ``out`` = (q_out, k_out) to reuse; returns them."""
     x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
     n, _, D = x.shape
+    _same_tokens(n, D, k=k)
     if out is None:
         out = _made(stream, lambda: (_dense(q), _dense(k)))
-    _m.msa_qk_norm_rope(dt_code(x), n, _heads(q), _heads(k), D, q, k, q_weight, k_weight, positions, eps,
-                        rope_base, *out, stream)
+    _m.msa_qk_norm_rope(dt_code(x), n, _heads(q), _heads(k), D, q, k, q_weight, k_weight,
+                        positions, eps, rope_base, *out, stream)
     return out
 
 
@@ -375,7 +386,13 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     None).  ``out``: the four to reuse (dq and dk may be slices, as q and k).
     ``ws``: from qk_norm_rope_backward_workspace (made here if None)."""
     x, dy = (q, dq_out) if q is not None else (k, dk_out)
+    if x is None:
+        raise ValueError("q and k are both None")
     n, _, D = x.shape
+    for what, t, g in (("q", q, dq_out), ("k", k, dk_out)):
+        if (t is None) != (g is None) or (t is not None and g.shape != t.shape):
+            raise ValueError(f"d{what}_out has the shape of {what}, or is None with it")
+    _same_tokens(n, D, k=k)
 
     def grad(t, w):
         return None if t is None or w is None else torch.empty_like(w, dtype=torch.float32)
@@ -385,9 +402,9 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     if out is None:
         out = _made(stream, lambda: (_dense(dq_out), _dense(dk_out), grad(q, q_weight),
                                      grad(k, k_weight)))
-    _m.msa_qk_norm_rope_backward(dt_code(x), dt_code(dy), n, _heads(q), _heads(k), D, q, k, q_weight, k_weight,
-                                 positions, eps, rope_base, dq_out, dk_out, *out, ws,
-                                 0 if ws is None else ws.numel(), stream)
+    _m.msa_qk_norm_rope_backward(dt_code(x), dt_code(dy), n, _heads(q), _heads(k), D, q, k,
+                                 q_weight, k_weight, positions, eps, rope_base, dq_out, dk_out,
+                                 *out, ws, 0 if ws is None else ws.numel(), stream)
     return out
 
 
@@ -436,6 +453,7 @@ class PagedCache:
         queries ``q`` [N][Hq][D], norms and rotates them in the same launch
         and returns them (``q_out``, made here if None)."""
         n = k.shape[0]
+        _same_tokens(n, self.D, q=q)
         if q is not None and q_out is None:
             q_out = _made(stream, lambda: _dense(q))
         _m.msa_paged_append(dt_code(k), self.B, n, _heads(q), self.H, self.D, q, k, v, q_weight,
@@ -464,6 +482,8 @@ class TreeAttention:
         if (cache.B, cache.H, cache.D) != (B, H, D):
             raise ValueError(f"the cache holds {cache.B} x {cache.H} x {cache.D}, "
                              f"the attention was made for {B} x {H} x {D}")
+        if q.shape[1:] != (Hq, D):
+            raise ValueError(f"q has shape {tuple(q.shape)}, needs [n, {Hq}, {D}]")
         if out is None:
             out = _made(stream, lambda: _dense(q))
         _m.msa_tree_attn(self.dt, B, q.shape[0], n_max, Hq, H, D, q, tok_offsets, parents, k_mem,

@@ -197,6 +197,33 @@ def test_binding_refuses_other_layouts(stub):
     assert stub.calls == []
 
 
+def test_binding_refuses_operands_of_different_lengths(stub):
+    """What a call left out would come back as uninitialised rows."""
+    pos, off = torch.zeros(6, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    q, k, k6 = torch.zeros(5, 4, 64), torch.zeros(5, 2, 64), torch.zeros(6, 2, 64)
+    with pytest.raises(ValueError, match="both None"):
+        pipeline.qk_norm_rope(None, None, pos)
+    with pytest.raises(ValueError, match="both None"):
+        pipeline.qk_norm_rope_backward(None, None, pos, None, None)
+    with pytest.raises(ValueError, match="k has shape"):
+        pipeline.qk_norm_rope(q, k6, pos)
+    with pytest.raises(ValueError, match="k has shape"):
+        pipeline.qk_norm_rope_backward(q, k6, pos, q, k6)
+    with pytest.raises(ValueError, match="dk_out has the shape of k"):
+        pipeline.qk_norm_rope_backward(q, k, pos, q, k6)
+    with pytest.raises(ValueError, match="dk_out has the shape of k"):
+        pipeline.qk_norm_rope_backward(q, k, pos, q, None)
+    with pytest.raises(ValueError, match="dq_out has the shape of q"):
+        pipeline.qk_norm_rope_backward(None, k, pos, q, k)
+    c = pipeline.PagedCache(torch.float32, 4, 16, 2, 64, 2, 3, "cpu")
+    with pytest.raises(ValueError, match="q has shape"):
+        c.append(k, k, off, pos, q=torch.zeros(6, 4, 64))
+    att = pipeline.TreeAttention(torch.float32, 2, 4, 4, 2, 64, 0, 3, 16, "cpu")
+    with pytest.raises(ValueError, match="q has shape"):
+        att(torch.zeros(5, 8, 64), off, c)
+    assert [n for n, _ in stub.calls] == ["msa_tree_attn_workspace_size"]
+
+
 def test_binding_refuses_a_cache_of_other_sizes(stub):
     c = pipeline.PagedCache(torch.float32, 4, 16, 2, 64, 2, 3, "cpu")
     off, pos = torch.zeros(3, dtype=torch.int64), torch.zeros(5, dtype=torch.int32)

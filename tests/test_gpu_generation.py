@@ -904,7 +904,7 @@ def test_debug_library_refuses_bad_arrays(cuda_device):
     from latent_memory_routing_b200 import build
     build.build(debug=True)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD], cwd=root, capture_output=True, text=True,
-                       env=dict(os.environ, MSA_DEBUG="1"), timeout=600)
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD], cwd=root, capture_output=True,
+                       text=True, env=dict(os.environ, MSA_DEBUG="1"), timeout=600)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     assert "debug build ok" in r.stdout
