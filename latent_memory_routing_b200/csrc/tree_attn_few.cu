@@ -12,7 +12,7 @@
 // one token each: 114 us in tree_attn_tc.cu, 103 here with the merge, 5.8
 // TB/s); here every warp is a worker of its own:
 //   * The 16-key slices of all (sequence, KV head) items stand in one line,
-//     cut into one contiguous range a warp.  An item inside one range is
+//     cut into one contiguous range a worker (neighbours on different SMs).  An item inside one range is
 //     written directly, one cut by a border as fp32 partials (at most two a
 //     warp) that a second launch merges in a fixed order.
 //   * A warp's lane 0 copies slices of K and V by TMA into the warp's own ring
@@ -39,7 +39,7 @@ namespace {
 constexpr int kSlice = 16;                // keys of a slice
 constexpr int kWarps = 8;                 // workers of a CTA, one CTA an SM
 constexpr int kFewThreads = 32 * kWarps;
-constexpr int kMinRange = 6;
+constexpr float kWholeItem = 8.f, kSqRange = 128.f;  // slices of an item
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D> struct FC {
@@ -143,6 +143,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   // The slices of all sequences, a run of sequences a thread, scanned over
   // the CTA's threads.
   const int per = (a.B + kFewThreads - 1) / kFewThreads;
+  int64_t items;
   {
     int64_t mine = 0;
     for (int b = min(a.B, tid * per); b < min(a.B, (tid + 1) * per); ++b) {
@@ -151,6 +152,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       aux.seq[tid] = s;
       mine += (int64_t)seq_slices(s) * a.H;
     }
+    items = (int64_t)(per == 1 ? __syncthreads_count(mine > 0) : a.B) * a.H;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,11 +173,18 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     __syncthreads();
   }
   const int64_t total = aux.pre[kFewThreads];
-  const int64_t worker = (int64_t)blockIdx.x * kWarps + warp;
-  // ranges of about kMinRange slices at least: shorter ones would end sooner
-  // but leave more parts to merge
-  const int64_t n_work =
-      min((int64_t)gridDim.x * kWarps, (total + kMinRange - 1) / kMinRange);
+  const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x;  // few: on as many SMs
+  // Short items stay whole, a worker each.  Of a long one a range costs its
+  // length and the merge their number, so the least length goes with the root
+  // of the item's; one slice is too little where that would fill every worker.
+  // (33 sequences of 9 keys: 33 us with ranges of 6 slices at least, 10; one
+  // item of 125 slices: 14 with 6, 10.5; of 1,000: 18 with ranges of one, 14.)
+  const int64_t all = (int64_t)gridDim.x * kWarps;
+  const float mean = (float)total / (float)max(items, (int64_t)1);
+  const int64_t least =
+      max((int64_t)(total <= all ? 1 : 3), (int64_t)ceilf(sqrtf(mean / kSqRange)));
+  const int64_t n_work = min(
+      all, mean <= kWholeItem ? min(items, total) : (total + least - 1) / least);
   auto range_lo = [&](int64_t i) { return i * total / n_work; };
   const int64_t lo = worker < n_work ? range_lo(worker) : 0;
   const int64_t hi = worker < n_work ? range_lo(worker + 1) : 0;

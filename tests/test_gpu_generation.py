@@ -452,6 +452,16 @@ def test_many_short_sequences(dt, Hq, n):
     status()
 
 
+@pytest.mark.parametrize("lens,toks,H", [([3] * 33, [6] * 33, 2), ([1, 0, 90, 7, 33, 5], [3] * 6, 4),
+                                         ([130], [2], 1), ([2000], [1], 1), ([4100, 5], [1, 4], 2),
+                                         ([20000], [1], 1)])
+def test_few_rows_over_short_and_long_items(lens, toks, H):
+    """Items kept whole, and cut into ranges of one slice and of more."""
+    t = tree_case(BF16, 16, 2 * H, H, 64, lens, toks, [], "chain", seed=3)
+    check_tree(t, run_tree(t, max(toks)))
+    status()
+
+
 @pytest.mark.parametrize("n_max", [1, 4, 5, 8, 9, 32, 33, 100, 128])
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_row_counts_around_the_kernels_tiles(dt, n_max):
