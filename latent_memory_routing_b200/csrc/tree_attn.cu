@@ -12,11 +12,11 @@
 // Queries and cached keys are already rotated (msa_paged_append); memory
 // rows keep their document-wise rotation.
 //
-// This file holds the fp32 kernels and the entry point; bf16 goes to
-// tree_attn_few.cu and tree_attn_tc.cu.  fp32 stays on the CUDA cores (the
-// tensor cores would round the operands): 4 D operations a row and key, bound
-// by the fp32 pipe for many rows and by latency for the small calls.  One CTA
-// per (split of a sequence's keys, block of query rows = tokens x heads of a KV
+// This file holds the fp32 kernels on the CUDA cores and the entry point; bf16
+// goes to tree_attn_few.cu and tree_attn_tc.cu, long fp32 calls of few rows to
+// the first too (in split tf32).  4 D operations a row and key: bound by the
+// fp32 pipe for many rows and by latency for the small calls.  One CTA per
+// (split of a sequence's keys, block of query rows = tokens x heads of a KV
 // group, KV head), tiles of keys copied ahead by cp.async, one pass with a
 // running maximum and sum; a second launch joins the splits.
 //   * up to 32 rows (tree_simt_kernel): 4 RW rows, a key a lane, RW rows a
@@ -550,6 +550,24 @@ int dispatch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s
                     static_cast<const float2*>(part_ml));
 }
 
+// Whether tree_attn_few.cu takes a call, by the rows R of a KV head.  bf16: one
+// row tile of 16 (with two, 17 to 32 rows, a slice took a warp so long that
+// loads waited: 16 sequences x 8,220 keys, 32 rows, 125 us against
+// tree_attn_tc.cu's 103 for 36; 64 sequences x 100 keys 46 us against 24).
+// fp32: two tiles, once there are 2e7 products of a row and a key's element in
+// the lengths that the buffers allow: its slices and merge take 11 to 14 us at
+// the least, where tree_simt_kernel takes 6 to 9 (2 sequences of 16 tokens
+// over 322 keys, 5e6 products: 12.3 against 9.0; 4 sequences x 4,104 keys, 4 /
+// 16 / 32 rows, 1.7e7 to 1.3e8: 23.6 / 26 / 36 against 23.1 / 28 / 41; 8 x
+// 32,104 keys: 143 / 147 / 273 against 218 / 448 / 742).
+bool takes_few(msa_dtype dt, int B, int n_max, int Hq, int H, int D, int m_cap, int max_pages,
+               int page_size) {
+  const int rows = n_max * (Hq / H);
+  if (dt == MSA_BF16) return rows <= 16;
+  const double keys = (double)m_cap + (double)max_pages * page_size;
+  return rows <= 32 && (double)rows * B * H * keys * D > 2e7;
+}
+
 // Shape checks shared by the call and its workspace size; a MSA status.
 int tree_shape(msa_dtype dt, int B, int n_max, int Hq, int H, int D, int m_cap, int max_pages,
                int page_size) {
@@ -612,13 +630,13 @@ int tree_body(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int 
   a.out = out;
   a.status = device_status_ptr();
   const TreePlan p = tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size);
-  const bool few = tree_few_takes(n_max, a.G);
-  const size_t need = dt == MSA_F32 ? p.total
-                      : few         ? tree_few_workspace_size(n_max, a.G, D)
-                                    : tree_tc_workspace_size(n_max, a.G, D);
+  const bool few = takes_few(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size);
+  const size_t need = few               ? tree_few_workspace_size(n_max, a.G, D)
+                      : dt == MSA_F32 ? p.total
+                                      : tree_tc_workspace_size(n_max, a.G, D);
   if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MSA_ERR_WORKSPACE;
-  if (dt == MSA_BF16)
-    return few ? tree_few_launch(a, D, ws, s) : tree_tc_launch(a, D, ws, s);
+  if (few) return tree_few_launch(dt, a, D, ws, s);
+  if (dt == MSA_BF16) return tree_tc_launch(a, D, ws, s);
   return D == 64 ? dispatch_simt<64>(a, p, ws, s) : dispatch_simt<128>(a, p, ws, s);
 }
 
@@ -629,9 +647,9 @@ extern "C" size_t msa_tree_attn_workspace_size(msa_dtype dt, int B, int n_max, i
                                                int D, int m_cap, int max_pages, int page_size) {
   using namespace msa;
   if (tree_shape(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size)) return 0;
-  if (dt == MSA_BF16)
-    return tree_few_takes(n_max, Hq / H) ? tree_few_workspace_size(n_max, Hq / H, D)
-                                         : tree_tc_workspace_size(n_max, Hq / H, D);
+  if (takes_few(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size))
+    return tree_few_workspace_size(n_max, Hq / H, D);
+  if (dt == MSA_BF16) return tree_tc_workspace_size(n_max, Hq / H, D);
   return tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size).total;
 }
 

@@ -147,17 +147,17 @@ struct TreeCut {
   int g, row0, rows, last;  // last < 0: nothing to merge here
 };
 
-// Merges the bf16 partials of ctas x per workers (per <= 32) in a fixed order
-// (tree_attn_merge.cu): part (worker, slot) holds part_rows rows of fp32 O and
-// (max, sum) in the base-2 domain.
-int tree_merge_launch(const TreeArgs& a, int D, int ctas, int per, int part_rows,
+// Merges the partials of ctas x per workers in a fixed order, into outputs in
+// fp32 or bf16 (tree_attn_merge.cu): part (worker, slot) holds part_rows rows
+// of fp32 O and (max, sum) in the base-2 domain.
+int tree_merge_launch(const TreeArgs& a, bool f32, int D, int ctas, int per, int part_rows,
                       const float* part_o, const float2* part_ml, const TreeCut* cuts,
                       cudaStream_t s);
 
-// bf16, n_max G <= 16 rows a KV head: a warp a worker (tree_attn_few.cu).
-bool tree_few_takes(int n_max, int G);
+// Few rows a KV head (16 in bf16, 32 in fp32): a warp a worker
+// (tree_attn_few.cu).
 size_t tree_few_workspace_size(int n_max, int G, int D);
-int tree_few_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);
+int tree_few_launch(msa_dtype dt, const TreeArgs& a, int D, void* ws, cudaStream_t s);
 
 // bf16 on tcgen05 (tree_attn_tc.cu): any shape the entry point takes.
 size_t tree_tc_workspace_size(int n_max, int G, int D);

@@ -1,9 +1,10 @@
-// bf16 attention for drafted token trees over [memory ; paged cache ; drafted
+// Attention for drafted token trees over [memory ; paged cache ; drafted
 // tokens] when a KV head has few query rows (method and semantics:
-// tree_attn.cu): plain decode and small trees, R = n G <= 16 rows.
+// tree_attn.cu): plain decode and small trees, R = n G <= 16 rows in bf16, 32
+// in fp32 (two items of 16).
 //
 // Mathematics.  As tree_attn_tc.cu: S = Q K^T, p = 2^(scale log2(e) s - m),
-// O += bf16(p) V, l += p, one pass over the keys.
+// O += p V (p in bf16 with bf16 values), l += p, one pass over the keys.
 //
 // What bounds it.  4 D bytes a key and KV head against 4 R D operations: HBM,
 // by far, so all that matters is bytes in flight and what happens at the ends
@@ -12,9 +13,10 @@
 // one token each: 114 us in tree_attn_tc.cu, 103 here with the merge, 5.8
 // TB/s); here every warp is a worker of its own:
 //   * The 16-key slices of all (sequence, KV head) items stand in one line,
-//     cut into one contiguous range a worker (neighbours on different SMs).  An item inside one range is
-//     written directly, one cut by a border as fp32 partials (at most two a
-//     warp) that a second launch merges in a fixed order.
+//     cut into one contiguous range a worker (neighbours on different SMs).
+//     An item inside one range is written directly, one cut by a border as
+//     fp32 partials (at most two a warp) that a second launch merges in a
+//     fixed order.
 //   * A warp's lane 0 copies slices of K and V by TMA into the warp's own ring
 //     (a slice never crosses a page: pages hold a multiple of 16 rows), waits
 //     on its own barriers, and no warp waits for another.
@@ -26,6 +28,9 @@
 //     rows, unseen scores become -inf, V rows past the end zero, and
 //     non-finite drafted values are taken out of V (0 times them would reach
 //     every row) and added at the end for the rows that see them.
+//   * fp32 takes slices of 8 keys on m16n8k8, operands split into two tf32
+//     terms: 96 instructions a slice of 8 KB, which bound it (8 sequences x
+//     32,104 keys: 143 us, 3.7 TB/s; with a third of the products 91 us, 5.8).
 #include <algorithm>
 #include <cmath>
 
@@ -36,15 +41,17 @@
 namespace msa {
 namespace {
 
-constexpr int kSlice = 16;                // keys of a slice
 constexpr int kWarps = 8;                 // workers of a CTA, one CTA an SM
 constexpr int kFewThreads = 32 * kWarps;
 constexpr float kWholeItem = 8.f, kSqRange = 128.f;  // slices of an item
 constexpr float kRescaleLog2 = 8.f;
 
-template <int D> struct FC {
-  static constexpr int KB = D / 64;                 // 64-dim blocks of a slice
-  static constexpr int BLK = kSlice * 128;          // 2 KB
+template <typename T, int D> struct FC {
+  static constexpr bool F32 = sizeof(T) == 4;
+  static constexpr int SL = F32 ? 8 : 16;           // keys of a slice
+  static constexpr int NT = SL / 8;                 // 8-key tiles of S
+  static constexpr int KB = D * sizeof(T) / 128;    // 128-byte blocks of a row
+  static constexpr int BLK = SL * 128;
   static constexpr int SLICE = 2 * KB * BLK;        // K and V of a slice
   static constexpr int DEPTH = 24576 / SLICE;       // slices in flight: 24 KB a warp
   static constexpr size_t SMEM = 1024 + (size_t)kWarps * DEPTH * SLICE;
@@ -89,24 +96,224 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int slices(int rows) { return (rows + kSlice - 1) / kSlice; }
-__device__ __forceinline__ int seq_slices(const TreeSeq& s) {
-  return s.n == 0 ? 0 : slices(s.M) + slices(s.cache);
+// The same of tf32 operands (16 x 8, 8 x 8).
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                     uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo in tf32 (11 bits each): hi cut off, lo rounded, which leaves
+// 2^-21 of x.  Integer instructions: the conversion's rate is a quarter of
+// theirs (8 x 32,100 keys, 8 / 2 heads, a token: 167 us with it, 143).  A NaN
+// stays one in hi; an infinity becomes inf + (-0).
+__device__ __forceinline__ uint32_t low32(float x, uint32_t hi) {
+  return (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+}
+__device__ __forceinline__ void split32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = low32(x, hi);
+}
+// The same, in its place: not taken out of the loop over slices (where 128
+// dims of 16 rows would fill the registers).
+__device__ __forceinline__ void split32_here(float x, uint32_t& hi, uint32_t& lo) {
+  asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(hi) : "r"(__float_as_uint(x)));
+  lo = low32(x, hi);
+}
+__device__ __forceinline__ float4 lds128(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
-// A worker's place in its range: slice j of item (b, g); `left` slices of the
-// range from here on.
-struct Cursor {
+// The products of a slice with the 16 rows of a warp.  Lane (g, t) = (lane /
+// 4, lane % 4) holds S and p of rows g and g + 8 at keys 8 n + 2 t, + 1 (the
+// instruction's layout), and of O the columns col(d, x) below.
+template <typename T, int D> struct Rows;
+
+template <int D> struct Rows<__nv_bfloat16, D> {
+  using C = FC<__nv_bfloat16, D>;
+  uint32_t q[D / 16][4];
+  __device__ __forceinline__ void load(const void* base, int64_t row, int h, bool on, int lane) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + row * D + 2 * (lane & 3);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      q[kk][h] = on ? *reinterpret_cast<const uint32_t*>(p + kk * 16) : 0u;
+      q[kk][2 + h] = on ? *reinterpret_cast<const uint32_t*>(p + kk * 16 + 8) : 0u;
+    }
+  }
+  __device__ __forceinline__ void scores(uint32_t kb_u, int lane, float (&sc)[C::NT][4]) const {
+    // ldmatrix: this lane's row and 16-byte piece of a 16 x 16 block
+    const int kr = ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sc[t][x] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t b[4];
+      ldsm4(kb_u + (kk >> 2) * C::BLK + kr * 128 + (((2 * (kk & 3) + kc) ^ (kr & 7)) << 4), b);
+      mma16(sc[0], q[kk], b[0], b[1]);
+      mma16(sc[1], q[kk], b[2], b[3]);
+    }
+  }
+  __device__ __forceinline__ static void add(uint32_t vb_u, int lane, const float (&p)[C::NT][4],
+                                             float (&o)[D / 8][4]) {
+    const int vr = (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
+    const uint32_t pf[4] = {pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]),
+                            pack2(p[1][0], p[1][1]), pack2(p[1][2], p[1][3])};
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      uint32_t b[4];
+      ldsm4t(vb_u + (d >> 2) * C::BLK + vr * 128 + (((2 * (d & 3) + vc) ^ (vr & 7)) << 4), b);
+      mma16(o[2 * d], pf, b[0], b[1]);
+      mma16(o[2 * d + 1], pf, b[2], b[3]);
+    }
+  }
+  __device__ __forceinline__ static int col(int d, int x, int lane) {
+    return 8 * d + 2 * (lane & 3) + x;
+  }
+};
+
+// fp32: every operand as two tf32 terms, three of the four products: each
+// factor's rest is 2^-21 of it at most, lo lo 2^-20 of the product (a few 2^-24
+// on the average), and sums are in fp32.  An infinity among the keys or values
+// that a row sees may make it NaN (inf 0).  The order of dims and columns is
+// free, and chosen so that a lane reads 16 bytes at a time without bank
+// conflicts: its dims of a 32-dim block are 8 t .. 8 t + 7, its columns of V
+// 4 g .. 4 g + 3.
+template <int D> struct Rows<float, D> {
+  using C = FC<float, D>;
+  float4 q[D / 16][2];
+  __device__ __forceinline__ void load(const void* base, int64_t row, int h, bool on, int lane) {
+    const float* p = static_cast<const float*>(base) + row * D + 8 * (lane & 3);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      q[c][h] = on ? *reinterpret_cast<const float4*>(p + 32 * (c >> 1) + 4 * (c & 1))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void scores(uint32_t kb_u, int lane, float (&sc)[C::NT][4]) const {
+    const int g = lane >> 2, t = lane & 3;
+    float s3[3][2][4];  // six chains of sums
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s3[i][y][x] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const float4 k = lds128(kb_u + (c >> 1) * C::BLK + g * 128 + (((2 * t + (c & 1)) ^ g) << 4));
+      const float kf[4] = {k.x, k.y, k.z, k.w};
+      const float q0[4] = {q[c][0].x, q[c][0].y, q[c][0].z, q[c][0].w};
+      const float q1[4] = {q[c][1].x, q[c][1].y, q[c][1].z, q[c][1].w};
+      uint32_t kh[4], kl[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) split32(kf[x], kh[x], kl[x]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t ah[4], al[4];
+        const float f[4] = {q0[2 * y], q1[2 * y], q0[2 * y + 1], q1[2 * y + 1]};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if constexpr (D == 128)
+            split32_here(f[x], ah[x], al[x]);
+          else
+            split32(f[x], ah[x], al[x]);
+        mma8(s3[0][y], ah, kh[2 * y], kh[2 * y + 1]);
+        mma8(s3[1][y], ah, kl[2 * y], kl[2 * y + 1]);
+        mma8(s3[2][y], al, kh[2 * y], kh[2 * y + 1]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      sc[0][x] = (s3[0][0][x] + s3[0][1][x]) +
+                 ((s3[1][0][x] + s3[1][1][x]) + (s3[2][0][x] + s3[2][1][x]));
+  }
+  __device__ __forceinline__ static void add(uint32_t vb_u, int lane, const float (&p)[C::NT][4],
+                                             float (&o)[D / 8][4]) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t ph[4], pl[4];  // its keys 2 t and 2 t + 1 stand for t and t + 4
+    split32(p[0][0], ph[0], pl[0]);
+    split32(p[0][2], ph[1], pl[1]);
+    split32(p[0][1], ph[2], pl[2]);
+    split32(p[0][3], ph[3], pl[3]);
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m) {
+      const uint32_t at = vb_u + m * C::BLK + 2 * t * 128;
+      const float4 v0 = lds128(at + ((g ^ (2 * t)) << 4));
+      const float4 v1 = lds128(at + 128 + ((g ^ (2 * t + 1)) << 4));
+      const float f0[4] = {v0.x, v0.y, v0.z, v0.w}, f1[4] = {v1.x, v1.y, v1.z, v1.w};
+      uint32_t h0[4], l0[4], h1[4], l1[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        split32(f0[x], h0[x], l0[x]);
+        split32(f1[x], h1[x], l1[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma8(o[4 * m + x], ph, h0[x], h1[x]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma8(o[4 * m + x], ph, l0[x], l1[x]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma8(o[4 * m + x], pl, h0[x], h1[x]);
+    }
+  }
+  __device__ __forceinline__ static int col(int d, int x, int lane) {
+    return 32 * (d >> 2) + 8 * (lane & 3) + 4 * x + (d & 3);
+  }
+};
+
+// 32 bits of V with non-finite values replaced by 0.
+template <typename T> __device__ __forceinline__ uint32_t finite(uint32_t w) {
+  if constexpr (sizeof(T) == 4)
+    return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+  else
+    return finite_bf16x2(w);
+}
+
+template <typename T> __device__ __forceinline__ float ex2(float x) {
+  if constexpr (sizeof(T) == 4)
+    return exp2f(x);
+  else
+    return ex2a(x);
+}
+
+// Slices of a sequence's item; its items are its KV heads' rows, 16 at a time.
+template <typename T> __device__ __forceinline__ int slices(int rows) {
+  constexpr int SL = FC<T, 64>::SL;
+  return (rows + SL - 1) / SL;
+}
+template <typename T> __device__ __forceinline__ int seq_slices(const TreeSeq& s) {
+  return s.n == 0 ? 0 : slices<T>(s.M) + slices<T>(s.cache);
+}
+template <typename T>
+__device__ __forceinline__ int row_tiles(const TreeArgs& a, const TreeSeq& s) {
+  return FC<T, 64>::F32 ? (s.n * a.G + 15) / 16 : 1;
+}
+
+// A worker's place in its range: slice j of item i of sequence b; `left`
+// slices of the range from here on.
+template <typename T> struct Cursor {
   TreeSeq s;
-  int b, g, j, nt;
+  int b, i, j, nt;
   int64_t left;
-  __device__ __forceinline__ void size() { nt = seq_slices(s); }
+  __device__ __forceinline__ void size() { nt = seq_slices<T>(s); }
+  // The KV head and the first row of item i.
+  __device__ __forceinline__ int g(const TreeArgs& a) const { return i / row_tiles<T>(a, s); }
+  __device__ __forceinline__ int row0(const TreeArgs& a) const {
+    return i % row_tiles<T>(a, s) * 16;
+  }
   // To slice 0 of the next item that has any (only while left > 0).
   template <typename Seq>
-  __device__ __forceinline__ void next_item(int H, Seq seq) {
+  __device__ __forceinline__ void next_item(const TreeArgs& a, Seq seq) {
     j = 0;
-    if (++g < H) return;
-    g = 0;
+    if (++i < a.H * row_tiles<T>(a, s)) return;
+    i = 0;
     do {
       s = seq(++b);
       size();
@@ -114,7 +321,7 @@ struct Cursor {
   }
 };
 
-template <int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(kFewThreads, 1)
 tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                 const __grid_constant__ CUtensorMap tm_vm,
@@ -122,7 +329,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ TreeArgs a,
                 int part_rows, float* __restrict__ part_o, float2* __restrict__ part_ml,
                 TreeCut* __restrict__ cuts) {
-  using C = FC<D>;
+  using C = FC<T, D>;
   pdl_trigger();  // the merge: its blocks come as this grid's leave
   pdl_wait();
   extern __shared__ __align__(1024) unsigned char dsm[];
@@ -146,13 +353,18 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   int64_t items;
   {
     int64_t mine = 0;
+    int tiles = 0;
     for (int b = min(a.B, tid * per); b < min(a.B, (tid + 1) * per); ++b) {
       const TreeSeq s = tree_seq(a, b);
       if (s.error && blockIdx.x == 0) record_error(a.status, s.error);
       aux.seq[tid] = s;
-      mine += (int64_t)seq_slices(s) * a.H;
+      tiles = seq_slices<T>(s) > 0 ? row_tiles<T>(a, s) : 0;
+      mine += (int64_t)seq_slices<T>(s) * a.H * tiles;
     }
-    items = (int64_t)(per == 1 ? __syncthreads_count(mine > 0) : a.B) * a.H;
+    // (more sequences than threads: at least as many as there are, about)
+    items = per == 1 ? __syncthreads_count(tiles > 0) : a.B;
+    if (C::F32 && per == 1) items += __syncthreads_count(tiles > 1);
+    items *= a.H;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -200,7 +412,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     if (per == 1) return aux.seq[b];
     return tree_seq(a, b);
   };
-  Cursor ld;  // the slice to load next
+  Cursor<T> ld;  // the slice to load next
   {
     // the last thread whose sequences begin at or before slice lo
     int t = 0;
@@ -213,17 +425,17 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     for (;;) {  // (its run holds lo, so this ends)
       ld.s = seq(ld.b);
       ld.size();
-      const int64_t n = (int64_t)ld.nt * a.H;
+      const int64_t n = (int64_t)ld.nt * a.H * row_tiles<T>(a, ld.s);
       if (lo < at + n || ld.b + 1 >= a.B) break;
       at += n;
       ++ld.b;
     }
     const int64_t off = lo - at;
-    ld.g = (int)(off / ld.nt);
-    ld.j = (int)(off - (int64_t)ld.g * ld.nt);
+    ld.i = (int)(off / ld.nt);
+    ld.j = (int)(off - (int64_t)ld.i * ld.nt);
     ld.left = hi - lo;
   }
-  Cursor cu = ld;  // the slice to compute next
+  Cursor<T> cu = ld;  // the slice to compute next
   if (ld.j > 0 && range_lo(worker - 1) <= lo - ld.j) {
     // the first border inside this item: its last part holds slice `end`
     const int64_t end = lo - ld.j + ld.nt - 1;
@@ -232,8 +444,9 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     while (range_lo(c) > end) --c;
     cut.last = (int)c;
     cut.t0 = ld.s.t0;
-    cut.g = ld.g;
-    cut.rows = ld.s.n * a.G;
+    cut.g = ld.g(a);
+    cut.row0 = ld.row0(a);
+    cut.rows = min(ld.s.n * a.G - cut.row0, 16);
   }
   if (lane == 0) cuts[worker] = cut;
 
@@ -243,18 +456,18 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   bool ids_fresh = true;
   auto issue = [&](int slot) {
     if (ld.left == 0) return;
-    const int n_ms = slices(ld.s.M);
+    const int n_ms = slices<T>(ld.s.M);
     if (ids_fresh || ld.j >= ids0 + 32) {
       ids0 = ld.j;
       ids = -1;
       const int j = ids0 + lane;
       if (j < n_ms) {
-        ids = ld.b * a.m_cap + j * kSlice;
+        ids = ld.b * a.m_cap + j * C::SL;
       } else if (j < ld.nt) {
-        const int r0 = (j - n_ms) * kSlice;
+        const int r0 = (j - n_ms) * C::SL;
         const int pg = a.block_table[(int64_t)ld.b * a.max_pages + r0 / a.page_size];
         if (pg >= 0 && pg < a.n_pages)
-          ids = (pg * a.H + ld.g) * a.page_size + r0 % a.page_size;
+          ids = (pg * a.H + ld.g(a)) * a.page_size + r0 % a.page_size;
         else
           record_error(a.status, MSA_ERR_INVALID_ARG);
       }
@@ -269,15 +482,15 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb) {
           tc::tma_load_3d(d + kb * C::BLK, mem ? &tm_km : &tm_kp, &full[slot], kb * 64,
-                          mem ? ld.g : 0, row);
+                          mem ? ld.g(a) : 0, row);
           tc::tma_load_3d(d + (C::KB + kb) * C::BLK, mem ? &tm_vm : &tm_vp, &full[slot], kb * 64,
-                          mem ? ld.g : 0, row);
+                          mem ? ld.g(a) : 0, row);
         }
       }
     }
     --ld.left;
     if (++ld.j == ld.nt && ld.left > 0) {
-      ld.next_item(a.H, seq);
+      ld.next_item(a, seq);
       ids_fresh = true;
     }
   };
@@ -287,9 +500,6 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   // ---------------------------------------------------------------- compute
   const int c2 = 2 * (lane & 3);  // this thread's columns of an 8-column tile
   const int r4 = lane >> 2;       // its rows of a 16-row tile: r4, r4 + 8
-  // ldmatrix: this lane's row and 16-byte piece of a 16 x 16 block
-  const int kr = ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
-  const int vr = (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
   const uint32_t ring_u = tc::smem_u32(ring);
   bool ok = true;
   int slot = 0;
@@ -297,21 +507,17 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   while (cu.left > 0 && ok) {
     // an item's share: its queries, trees, and slices
     const TreeSeq s = cu.s;
-    const int rows = s.n * a.G, n_ms = slices(s.M);
+    const int g = cu.g(a), row0 = cu.row0(a);
+    const int rows = min(s.n * a.G - row0, 16), n_ms = slices<T>(s.M);
     const int cnt = (int)min((int64_t)(cu.nt - cu.j), cu.left), j_lo = cu.j;
     const int part = j_lo > 0 ? 0 : cnt < cu.nt ? 1 : -1;
-    uint32_t qf[D / 16][4];
+    Rows<T, D> q;
     int64_t out_row[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = r4 + 8 * h;
-      out_row[h] = r < rows ? (s.t0 + r / a.G) * a.Hq + cu.g * a.G + r % a.G : (int64_t)-1;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + out_row[h] * D + c2;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qf[kk][h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16) : 0u;
-        qf[kk][2 + h] = r < rows ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 8) : 0u;
-      }
+      const int r = row0 + r4 + 8 * h;
+      out_row[h] = r4 + 8 * h < rows ? (s.t0 + r / a.G) * a.Hq + g * a.G + r % a.G : (int64_t)0;
+      q.load(a.q, out_row[h], h, r4 + 8 * h < rows, lane);
     }
     // ancestor sets, a lane a row
     __syncwarp();
@@ -326,9 +532,9 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       }
       __syncwarp();
     }
-    if (lane < rows) {  // at most 16 rows, so at most 16 tokens
+    if (lane < rows) {  // (a KV head's rows, so its tokens too, are 32 at most)
       uint32_t m = 0;
-      int x = lane / a.G;
+      int x = (row0 + lane) / a.G;
       if (a.parents) {
         do {
           m |= 1u << x;
@@ -355,29 +561,19 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     for (int i = 0; i < cnt; ++i) {
       const int j = j_lo + i;
       const bool mem = j < n_ms;
-      const int key0 = (mem ? j : j - n_ms) * kSlice;
+      const int key0 = (mem ? j : j - n_ms) * C::SL;
       const int n_rows = (mem ? s.M : s.cache) - key0;
-      const bool all = key0 + kSlice <= (mem ? s.M : s.L);  // every row sees every key
+      const bool all = key0 + C::SL <= (mem ? s.M : s.L);  // every row sees every key
       ok = tc::mbar_wait(&full[slot], ph);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t kb_u = ring_u + slot * C::SLICE, vb_u = kb_u + C::KB * C::BLK;
 
-      float sc[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[t][x] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t b[4];
-        ldsm4(kb_u + (kk >> 2) * C::BLK + kr * 128 + (((2 * (kk & 3) + kc) ^ (kr & 7)) << 4), b);
-        mma16(sc[0], qf[kk], b[0], b[1]);
-        mma16(sc[1], qf[kk], b[2], b[3]);
-      }
+      float sc[C::NT][4];
+      q.scores(kb_u, lane, sc);
       if (!all) {
         const int off = s.L - key0;  // column of the first drafted key
-        const uint32_t in = n_rows >= 16 ? 0xffffu : (1u << n_rows) - 1;  // n_rows >= 1
+        const uint32_t in = n_rows >= C::SL ? 0xffffu : (1u << n_rows) - 1;  // n_rows >= 1
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t vis = in;
@@ -389,7 +585,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
                                : 0u;
           }
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < C::NT; ++t)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               if (!((vis >> (8 * t + c2 + x)) & 1)) sc[t][2 * h + x] = -INFINITY;
@@ -397,16 +593,15 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
         // clean V: rows past the end, non-finite drafted values
         unsigned char* v = ring + slot * C::SLICE + C::KB * C::BLK;
         bool bad = false;
-        for (int c = lane; c < kSlice * D / 8; c += 32) {
-          const int r = (c & 127) >> 3;  // 128 pieces of 16 bytes a block
-          uint4* p = reinterpret_cast<uint4*>(v + (c >> 7) * C::BLK + (c & 127) * 16);
+        for (int c = lane; c < C::KB * C::SL * 8; c += 32) {
+          const int r = (c / 8) % C::SL;  // 8 pieces of 16 bytes a row of a block
+          uint4* p = reinterpret_cast<uint4*>(v + c * 16);
           if (r >= n_rows) {
             *p = make_uint4(0, 0, 0, 0);
           } else if (!mem && key0 + r >= s.L && s.n > 1) {
             const uint4 x = *p;
             const uint4 y =
-                make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z),
-                           finite_bf16x2(x.w));
+                make_uint4(finite<T>(x.x), finite<T>(x.y), finite<T>(x.z), finite<T>(x.w));
             if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
               *p = y;
               bad = true;
@@ -420,8 +615,8 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       float mx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]),
-                      fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+        mx[h] = fmaxf(sc[0][2 * h], sc[0][2 * h + 1]);
+        if constexpr (C::NT == 2) mx[h] = fmaxf(mx[h], fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
         mx[h] *= a.qscale;
@@ -429,8 +624,8 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       // the reference maximum moves only when a slice exceeds it by 2^8
       const bool g0 = mx[0] > m_ref[0] + kRescaleLog2, g1 = mx[1] > m_ref[1] + kRescaleLog2;
       if (__any_sync(0xffffffffu, g0 || g1)) {
-        const float al0 = !g0 ? 1.f : m_ref[0] == -INFINITY ? 0.f : ex2a(m_ref[0] - mx[0]);
-        const float al1 = !g1 ? 1.f : m_ref[1] == -INFINITY ? 0.f : ex2a(m_ref[1] - mx[1]);
+        const float al0 = !g0 ? 1.f : m_ref[0] == -INFINITY ? 0.f : ex2<T>(m_ref[0] - mx[0]);
+        const float al1 = !g1 ? 1.f : m_ref[1] == -INFINITY ? 0.f : ex2<T>(m_ref[1] - mx[1]);
         if (g0) m_ref[0] = mx[0];
         if (g1) m_ref[1] = mx[1];
         l[0] *= al0;
@@ -443,25 +638,19 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
           o[d][3] *= al1;
         }
       }
-      uint32_t pf[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float nm = m_ref[h] == -INFINITY ? 0.f : -m_ref[h];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2a(fmaf(sc[t][2 * h], a.qscale, nm));
-          const float p1 = ex2a(fmaf(sc[t][2 * h + 1], a.qscale, nm));
+        for (int t = 0; t < C::NT; ++t) {
+          const float p0 = ex2<T>(fmaf(sc[t][2 * h], a.qscale, nm));
+          const float p1 = ex2<T>(fmaf(sc[t][2 * h + 1], a.qscale, nm));
           l[h] += p0 + p1;
-          pf[2 * t + h] = pack2(p0, p1);
+          sc[t][2 * h] = p0;
+          sc[t][2 * h + 1] = p1;
         }
       }
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        uint32_t b[4];
-        ldsm4t(vb_u + (d >> 2) * C::BLK + vr * 128 + (((2 * (d & 3) + vc) ^ (vr & 7)) << 4), b);
-        mma16(o[2 * d], pf, b[0], b[1]);
-        mma16(o[2 * d + 1], pf, b[2], b[3]);
-      }
+      Rows<T, D>::add(vb_u, lane, sc, o);
       __syncwarp();  // every lane has read the slot
       issue(slot);
       if (++slot == C::DEPTH) {
@@ -472,7 +661,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     if (!ok) break;
 
     // write the item's share
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+    T* out = static_cast<T*>(a.out);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = r4 + 8 * h;
@@ -484,36 +673,45 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       if (anc == 0) lr = 0.f;  // pruned
       const int64_t prow = (worker * 2 + max(part, 0)) * part_rows + r;
       const float inv = lr == 0.f ? 0.f : part >= 0 ? 1.f : 1.f / lr;
+      // (a row without weight: its O may hold 0 times NaN)
+      auto at = [&](int d, int x) { return inv == 0.f ? 0.f : o[d][2 * h + x] * inv; };
+      if constexpr (C::F32) {
+        float* dst = part < 0 ? out + out_row[h] * D : part_o + prow * D;
 #pragma unroll
-      for (int d = 0; d < D / 8; ++d) {
-        // (a row without weight: its O may hold 0 times NaN)
-        const float x = inv == 0.f ? 0.f : o[d][2 * h] * inv;
-        const float y = inv == 0.f ? 0.f : o[d][2 * h + 1] * inv;
-        if (part < 0)
-          *reinterpret_cast<uint32_t*>(out + out_row[h] * D + d * 8 + c2) = pack2(x, y);
-        else
-          *reinterpret_cast<float2*>(part_o + prow * D + d * 8 + c2) = make_float2(x, y);
+        for (int d = 0; d < D / 8; d += 4)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            *reinterpret_cast<float4*>(dst + Rows<T, D>::col(d, x, lane)) =
+                make_float4(at(d, x), at(d + 1, x), at(d + 2, x), at(d + 3, x));
+      } else {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          const int col = Rows<T, D>::col(d, 0, lane);
+          if (part < 0)
+            *reinterpret_cast<uint32_t*>(out + out_row[h] * D + col) = pack2(at(d, 0), at(d, 1));
+          else
+            *reinterpret_cast<float2*>(part_o + prow * D + col) = make_float2(at(d, 0), at(d, 1));
+        }
       }
       if (part >= 0 && c2 == 0) part_ml[prow] = make_float2(m_ref[h], lr);
       if (!any_bad) continue;
       // drafted values taken out of V, added for the rows that see them
 #pragma unroll 1
       for (int t = 0; t < s.n; ++t) {
-        const int kr2 = s.L + t, j = n_ms + kr2 / kSlice;
+        const int kr2 = s.L + t, j = n_ms + kr2 / C::SL;
         if (!((anc >> t) & 1) || j < j_lo || j >= j_lo + cnt || kr2 >= s.cache) continue;
         const int pg = a.block_table[(int64_t)cu.b * a.max_pages + kr2 / a.page_size];
         if (pg < 0 || pg >= a.n_pages) continue;
-        const __nv_bfloat16* v =
-            static_cast<const __nv_bfloat16*>(a.v_pages) +
-            (((int64_t)pg * a.H + cu.g) * a.page_size + kr2 % a.page_size) * D;
+        const T* v = static_cast<const T*>(a.v_pages) +
+                     (((int64_t)pg * a.H + g) * a.page_size + kr2 % a.page_size) * D;
 #pragma unroll 1
         for (int d = 0; d < D / 4; ++d) {  // this thread's columns
-          const int col = 8 * (d >> 1) + c2 + (d & 1);
-          const float f = __bfloat162float(v[col]);
+          const int col = Rows<T, D>::col(d >> 1, d & 1, lane);
+          const float f = Elem<T>::to_f(v[col]);
           if (isfinite(f)) continue;
           if (part < 0) {
-            __nv_bfloat16* p = out + out_row[h] * D + col;
-            *p = __float2bfloat16(__bfloat162float(*p) + f);
+            T* p = out + out_row[h] * D + col;
+            *p = Elem<T>::from_f(Elem<T>::to_f(*p) + f);
           } else {
             part_o[prow * D + col] += f;
           }
@@ -522,7 +720,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     }
     cu.left -= cnt;
     cu.j += cnt;
-    if (cu.left > 0) cu.next_item(a.H, seq);
+    if (cu.left > 0) cu.next_item(a, seq);
   }
   if (!ok) {
     if (lane == 0) record_error(a.status, MSA_ERR_TIMEOUT);
@@ -543,7 +741,7 @@ struct FewPlan {
 };
 FewPlan few_plan(int n_max, int G, int D) {
   FewPlan p{};
-  p.part_rows = n_max * G;
+  p.part_rows = std::min(n_max * G, 16);
   const size_t parts = 2 * (size_t)num_sms() * kWarps * p.part_rows;
   p.po_bytes = round_up(parts * D * sizeof(float), 256);
   p.ml_bytes = round_up(parts * sizeof(float2), 256);
@@ -551,9 +749,10 @@ FewPlan few_plan(int n_max, int G, int D) {
   return p;
 }
 
-template <int D>
+template <typename T, int D>
 int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
-  using C = FC<D>;
+  using C = FC<T, D>;
+  constexpr int W = D * sizeof(T) / 2;  // a row in the maps' 16-bit units
   const FewPlan p = few_plan(a.n_max, a.G, D);
   unsigned char* w = static_cast<unsigned char*>(ws);
   float* part_o = reinterpret_cast<float*>(w);
@@ -561,34 +760,33 @@ int launch_few(const TreeArgs& a, void* ws, cudaStream_t s) {
   TreeCut* cuts = reinterpret_cast<TreeCut*>(w + p.po_bytes + p.ml_bytes);
   CUtensorMap km, vm, kp, vp;
   const int64_t page_rows = (int64_t)a.n_pages * a.H * a.page_size;
-  bool ok = tma_map_sw128_bf16(&kp, a.k_pages, D, 1, page_rows, 1, kSlice) &&
-            tma_map_sw128_bf16(&vp, a.v_pages, D, 1, page_rows, 1, kSlice);
+  bool ok = tma_map_sw128_bf16(&kp, a.k_pages, W, 1, page_rows, 1, C::SL) &&
+            tma_map_sw128_bf16(&vp, a.v_pages, W, 1, page_rows, 1, C::SL);
   if (a.m_cap > 0)
-    ok = ok && tma_map_sw128_bf16(&km, a.k_mem, D, a.H, (int64_t)a.B * a.m_cap, 1, kSlice) &&
-         tma_map_sw128_bf16(&vm, a.v_mem, D, a.H, (int64_t)a.B * a.m_cap, 1, kSlice);
+    ok = ok && tma_map_sw128_bf16(&km, a.k_mem, W, a.H, (int64_t)a.B * a.m_cap, 1, C::SL) &&
+         tma_map_sw128_bf16(&vm, a.v_mem, W, a.H, (int64_t)a.B * a.m_cap, 1, C::SL);
   else
     km = kp, vm = vp;  // never loaded from
   if (!ok) return note_cuda(cudaErrorInvalidValue);
-  auto kern = tree_few_kernel<D>;
+  auto kern = tree_few_kernel<T, D>;
   if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)C::SMEM)) return rc;
   const unsigned grid = (unsigned)num_sms();
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kFewThreads), C::SMEM, s, km, vm, kp, vp, a,
                           p.part_rows, part_o, part_ml, cuts))
     return rc;
-  return tree_merge_launch(a, D, (int)grid, kWarps, p.part_rows, part_o, part_ml, cuts, s);
+  return tree_merge_launch(a, C::F32, D, (int)grid, kWarps, p.part_rows, part_o, part_ml, cuts,
+                           s);
 }
 
 }  // namespace
 
-// One row tile of the warp's instructions.  (With two, 17 to 32 rows, a slice
-// took a warp so long that loads waited: 16 sequences x 8,220 keys, 32 rows,
-// 125 us against tree_attn_tc.cu's 103 for 36; 64 sequences x 100 keys 46 us
-// against 24.)
-bool tree_few_takes(int n_max, int G) { return n_max * G <= 16; }
 size_t tree_few_workspace_size(int n_max, int G, int D) { return few_plan(n_max, G, D).total; }
 
-int tree_few_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s) {
-  return D == 64 ? launch_few<64>(a, ws, s) : launch_few<128>(a, ws, s);
+int tree_few_launch(msa_dtype dt, const TreeArgs& a, int D, void* ws, cudaStream_t s) {
+  if (dt == MSA_F32)
+    return D == 64 ? launch_few<float, 64>(a, ws, s) : launch_few<float, 128>(a, ws, s);
+  return D == 64 ? launch_few<__nv_bfloat16, 64>(a, ws, s)
+                 : launch_few<__nv_bfloat16, 128>(a, ws, s);
 }
 
 }  // namespace msa

@@ -982,7 +982,7 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
   if (int rc = launch_pdl(kern, dim3(grid), dim3(kTcThreads), p.smem, s, qm, km, vm, kp, vp, a,
                           p.part_rows, p.tile_tok * a.G, p.q_rows, part_o, part_ml, cuts))
     return rc;
-  return tree_merge_launch(a, D, (int)grid, 1, p.part_rows, part_o, part_ml, cuts, s);
+  return tree_merge_launch(a, false, D, (int)grid, 1, p.part_rows, part_o, part_ml, cuts, s);
 }
 
 }  // namespace

@@ -462,6 +462,22 @@ def test_few_rows_over_short_and_long_items(lens, toks, H):
     status()
 
 
+@pytest.mark.parametrize("page,Hq,H,D,lens,toks,mem,tree,n_max", [
+    (16, 4, 2, 64, [6100, 0, 17], [16, 1, 5], [6, 0, 3], "tree", 16),
+    (32, 3, 3, 128, [40000, 31], [1, 1], [], "chain", 1),
+    (128, 5, 1, 64, [20000], [4], [130], "pruned", 5),
+    (64, 2, 2, 128, [5000, 12], [9, 17], [], "roots", 17),
+    (16, 16, 1, 128, [3000, 2999, 7, 0], [2, 1, 2, 0], [5, 0, 0, 9], "tree", 2),
+    (64, 8, 4, 64, [4000] * 3, [1, 3, 0], [], "chain", 8)])
+def test_long_fp32_items(page, Hq, H, D, lens, toks, mem, tree, n_max):
+    """One and two row tiles of 16, with padding tokens before and behind."""
+    t = tree_case(F32, page, Hq, H, D, lens, toks, mem, tree, seed=7, lead=3)
+    out = run_tree(t, n_max)
+    check_tree(t, out)
+    assert torch.equal(out.view(torch.int32), run_tree(t, n_max).view(torch.int32))
+    status()
+
+
 @pytest.mark.parametrize("n_max", [1, 4, 5, 8, 9, 32, 33, 100, 128])
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_row_counts_around_the_kernels_tiles(dt, n_max):
@@ -487,17 +503,18 @@ def test_padding_tokens_are_left_alone_and_scale_is_used(dt):
     status()
 
 
-@pytest.mark.parametrize("dt,D,n", [(F32, 64, 12), (F32, 64, 20), (BF16, 64, 8), (BF16, 64, 20),
-                                    (BF16, 128, 100)])
-def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n):
+@pytest.mark.parametrize("dt,D,n,rows", [(F32, 64, 12, 45), (F32, 64, 20, 45), (F32, 64, 8, 12005),
+                                         (F32, 64, 16, 7001), (BF16, 64, 8, 45),
+                                         (BF16, 64, 20, 45), (BF16, 128, 100, 45)])
+def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n, rows):
     """A drafted token's NaN or infinite K and V reach the rows that see it
     and no others."""
-    t = tree_case(dt, 16, 4, 2, D, [45], [n], [], "tree", seed=31)
+    t = tree_case(dt, 16, 4, 2, D, [rows], [n], [], "tree", seed=31)
     c, q, off, parents, *_ = t
     clean = run_tree(t, n)
     see = oracle.ancestors(parents.cpu().numpy())
     j = next(j for j in range(2, n) if 1 < see[:, j].sum() < n // 2)
-    pg, row = rows_of(c, 0, [45 + j])
+    pg, row = rows_of(c, 0, [rows + j])
     for poison_k, value in ((False, NAN), (False, float("inf")), (True, NAN)):
         keep = (c.k_pages if poison_k else c.v_pages)[pg, :, row].clone()
         (c.k_pages if poison_k else c.v_pages)[pg, :, row, :9] = value
