@@ -12,21 +12,16 @@
 // Queries and cached keys are already rotated (msa_paged_append); memory
 // rows keep their document-wise rotation.
 //
-// This file holds the fp32 kernels on the CUDA cores and the entry point; bf16
-// goes to tree_attn_few.cu and tree_attn_tc.cu, long fp32 calls of few rows to
-// the first too (in split tf32).  4 D operations a row and key: bound by the
+// This file holds the entry point and the kernel of small fp32 calls, on the
+// CUDA cores; bf16 goes to tree_attn_few.cu and tree_attn_tc.cu, the other fp32
+// calls to the first (in split tf32).  4 D operations a row and key: bound by the
 // fp32 pipe for many rows and by latency for the small calls.  One CTA per
 // (split of a sequence's keys, block of query rows = tokens x heads of a KV
 // group, KV head), tiles of keys copied ahead by cp.async, one pass with a
 // running maximum and sum; a second launch joins the splits.
-//   * up to 32 rows (tree_simt_kernel): 4 RW rows, a key a lane, RW rows a
-//     warp.  2 sequences of up to 16 tokens over 322 keys: 9 us (42 with
-//     scalar loads of one tile at a time and 64 keys a split).
-//   * above (tree_tile_kernel): 64 rows x 64 keys in register tiles of 4 x 4
-//     (4 x D / 16 of O), so that a value read from shared memory serves four
-//     products.  4 sequences of 64 tokens, 8 / 2 heads, over 4,164 keys: 389 us
-//     with a key a lane, 169 us so (26 TFLOP/s; one CTA of 8 warps an SM, the
-//     pipe busy about half of the time).
+// 4 RW rows a CTA, a key a lane, RW rows a warp: 2 sequences of up to 16
+// tokens over 322 keys, 9 us (42 with scalar loads of one tile at a time and 64
+// keys a split).
 #include <algorithm>
 #include <cmath>
 
@@ -39,11 +34,8 @@ constexpr int kThreads = 128;
 constexpr int kTile = 32;   // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kTileThreads = 256;
-constexpr int kBM = 64, kBN = 64;  // rows, keys of a register-tiled block
-
 struct TreePlan {
-  int rw;  // rows of a warp; 0: the register-tiled kernel
+  int rw;  // rows of a warp
   int n_blk, n_split;
   size_t po_bytes, ml_bytes, total;
 };
@@ -58,29 +50,12 @@ TreePlan tree_plan(int B, int n_max, int Hq, int H, int D, int m_cap, int max_pa
   const int rows_kv = n_max * (Hq / H);
   const int64_t keys = (int64_t)m_cap + (int64_t)max_pages * page_size;
   const int64_t want = 2LL * num_sms();
-  const int tile = rows_kv > 32 ? kBN : kTile;
-  const int64_t most = std::min<int64_t>((keys + tile - 1) / tile, 64);
-  p.rw = rows_kv > 32 ? 0 : rows_kv <= 4 ? 1 : rows_kv <= 8 ? 2 : rows_kv <= 16 ? 4 : 8;
+  const int64_t most = std::min<int64_t>((keys + kTile - 1) / kTile, 64);
+  p.rw = rows_kv <= 4 ? 1 : rows_kv <= 8 ? 2 : rows_kv <= 16 ? 4 : 8;
   for (;; p.rw /= 2) {
-    const int rows = p.rw ? 4 * p.rw : kBM;
-    p.n_blk = (rows_kv + rows - 1) / rows;
+    p.n_blk = (rows_kv + 4 * p.rw - 1) / (4 * p.rw);
     const int64_t base = (int64_t)B * H * p.n_blk;
     p.n_split = (int)std::max<int64_t>(1, std::min((want + base - 1) / base, most));
-    if (p.rw == 0) {
-      // one CTA an SM: the splits that fill their last round of SMs best, in
-      // four rounds at most (9 splits of 32 blocks, two rounds almost full,
-      // against 10, a third of 24 CTAs)
-      const int64_t sms = num_sms();
-      double best = 0.0;
-      for (int64_t ns = 1; ns <= most && (ns == 1 || base * ns <= 4 * sms); ++ns) {
-        const int64_t rounds = (base * ns + sms - 1) / sms;
-        const double fill = (double)(base * ns) / (double)(rounds * sms);
-        if (fill > best + 0.02) {
-          best = fill;
-          p.n_split = (int)ns;
-        }
-      }
-    }
     if (p.rw <= 1 || base * p.n_split >= num_sms()) break;
   }
   const size_t rows = (size_t)B * n_max * Hq;
@@ -282,208 +257,6 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int n_split, float* __restr
   }
 }
 
-template <int D> struct TileSmem {
-  float qs[kBM][D + 4];
-  float ks[2][kBN][D + 4];  // padded: 16 rows' 16-byte reads in two passes
-  float vs[2][kBN][D];
-  float ps[kBM][kBN + 4];
-  TreeMask mask;
-};
-
-// Many rows.  Thread (ty, tx) of 16 x 16 holds rows 4 ty .. of the block;
-// keys tx + 16 j of a tile in S, columns 4 tx + 64 j of O.
-template <int D>
-__global__ void __launch_bounds__(kTileThreads)
-tree_tile_kernel(const __grid_constant__ TreeArgs a, int n_split, float* __restrict__ part_o,
-                 float2* __restrict__ part_ml) {
-  constexpr int NC = D / 64;  // groups of 4 columns of O a thread holds
-  extern __shared__ __align__(16) unsigned char tile_raw[];
-  TileSmem<D>& sm = *reinterpret_cast<TileSmem<D>*>(tile_raw);
-  pdl_trigger();
-  pdl_wait();
-  const int split = blockIdx.x, blk = blockIdx.y;
-  const int b = blockIdx.z / a.H, g = blockIdx.z % a.H;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const TreeSeq s = tree_seq(a, b);
-  if (s.error && tid == 0) record_error(a.status, s.error);
-  const int G = a.G;
-  const int row0 = blk * kBM;
-  const int rows = min(kBM, s.n * G - row0);
-  if (rows <= 0) return;
-
-  const int keys = s.M + s.cache;
-  const int tiles = (keys + kBN - 1) / kBN;
-  const int t_lo = (int)((int64_t)split * tiles / n_split);
-  const int t_hi = (int)((int64_t)(split + 1) * tiles / n_split);
-  auto copy = [&](int t) {  // as tree_simt_kernel's
-    if (t < t_hi) {
-      const int j = tid >> 2, kk = t * kBN + j, d0 = (tid & 3) * 4;
-      const float *kp = static_cast<const float*>(a.k_pages),
-                  *vp = static_cast<const float*>(a.v_pages);
-      bool live = kk < keys;
-      if (live) {
-        int64_t off;
-        if (kk < s.M) {
-          kp = static_cast<const float*>(a.k_mem);
-          vp = static_cast<const float*>(a.v_mem);
-          off = (((int64_t)b * a.m_cap + kk) * a.H + g) * D;
-        } else {
-          const int slot = kk - s.M;
-          const int pg = a.block_table[(int64_t)b * a.max_pages + slot / a.page_size];
-          live = pg >= 0 && pg < a.n_pages;
-          if (!live && (tid & 3) == 0) record_error(a.status, MSA_ERR_INVALID_ARG);
-          off = live ? (((int64_t)pg * a.H + g) * a.page_size + slot % a.page_size) * D : 0;
-        }
-        kp += off;
-        vp += off;
-      }
-#pragma unroll
-      for (int d = 0; d < D; d += 16) {
-        cp16_or_zero(&sm.ks[t & 1][j][d + d0], kp + d + d0, live);
-        cp16_or_zero(&sm.vs[t & 1][j][d + d0], vp + d + d0, live);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  copy(t_lo);
-  for (int e = tid; e < kBM * (D / 4); e += kTileThreads) {
-    const int i = e / (D / 4), d = e % (D / 4) * 4, r = row0 + i;
-    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < rows)
-      q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                           ((s.t0 + r / G) * a.Hq + g * G + r % G) * D + d);
-    *reinterpret_cast<float4*>(&sm.qs[i][d]) =
-        make_float4(q.x * a.qscale, q.y * a.qscale, q.z * a.qscale, q.w * a.qscale);
-  }
-  tree_mask(a, s, sm.mask, tid, [] { __syncthreads(); });
-
-  float m_run[4], l_part[4], o[4][NC][4];
-  int tok[4];
-  bool alive[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m_run[i] = -INFINITY;
-    l_part[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[i][c][x] = 0.f;
-    const int r = 4 * ty + i;
-    tok[i] = r < rows ? (row0 + r) / G : 0;
-    alive[i] = r < rows && sm.mask.up[tok[i]] != kTreeDead;
-  }
-
-  for (int t = t_lo; t < t_hi; ++t) {
-    copy(t + 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
-    const float (*ks)[D + 4] = sm.ks[t & 1];
-    const float (*vs)[D] = sm.vs[t & 1];
-    float sc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
-#pragma unroll 2
-    for (int d = 0; d < D; d += 4) {
-      float4 q[4], k[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.qs[4 * ty + i][d]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(&ks[tx + 16 * j][d]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[i][j] = fmaf(
-              q[i].x, k[j].x,
-              fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, sc[i][j]))));
-    }
-    const bool all = (t + 1) * kBN <= s.M + s.L;  // every alive row sees every key
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!all) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kk = t * kBN + tx + 16 * j, dr = kk - s.M - s.L;
-          if (!(kk < keys && (dr < 0 || tree_bit(sm.mask.anc[tok[i]], dr)))) sc[i][j] = -INFINITY;
-        }
-      }
-      float mt = fmaxf(fmaxf(sc[i][0], sc[i][1]), fmaxf(sc[i][2], sc[i][3]));
-#pragma unroll
-      for (int x = 8; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-      const float m_new = fmaxf(m_run[i], mt);  // (NaN and -inf: as tree_simt_kernel)
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float corr = exp2f(m_run[i] - ref);
-      m_run[i] = m_new;
-      float ps = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(sc[i][j] - ref);
-        ps += p;
-        sm.ps[4 * ty + i][tx + 16 * j] = p;
-      }
-      l_part[i] = l_part[i] * corr + ps;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[i][c][x] *= corr;
-    }
-    __syncwarp();  // a row's 16 threads are in one warp
-#pragma unroll 2
-    for (int k = 0; k < kBN; k += 4) {
-      float p[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(&sm.ps[4 * ty + i][k]);
-        p[i][0] = f.x, p[i][1] = f.y, p[i][2] = f.z, p[i][3] = f.w;
-      }
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(&vs[k + y][4 * tx + 64 * c]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // weightless keys of a tile with unseen ones add nothing, NaN
-            // included
-            if (all || p[i][y] != 0.f) {
-              o[i][c][0] = fmaf(p[i][y], v.x, o[i][c][0]);
-              o[i][c][1] = fmaf(p[i][y], v.y, o[i][c][1]);
-              o[i][c][2] = fmaf(p[i][y], v.z, o[i][c][2]);
-              o[i][c][3] = fmaf(p[i][y], v.w, o[i][c][3]);
-            }
-          }
-        }
-    }
-    __syncthreads();  // the buffer may be copied into again
-  }
-
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
-    float l = l_part[i];
-#pragma unroll
-    for (int x = 8; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (r >= rows) continue;
-    if (!alive[i]) l = 0.f;  // pruned: weighs nothing
-    const int hq = g * G + (row0 + r) % G;
-    // no weight at all: zero; a NaN sum stays NaN
-    const float inv = n_split > 1 ? 1.f : 1.f / l;
-    const int64_t row = ((int64_t)b * a.n_max + tok[i]) * a.Hq + hq;
-    float* dst = n_split > 1
-                     ? part_o + (row * n_split + split) * D
-                     : static_cast<float*>(a.out) + ((s.t0 + tok[i]) * a.Hq + hq) * D;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      *reinterpret_cast<float4*>(dst + 4 * tx + 64 * c) =
-          l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                   : make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv,
-                                 o[i][c][3] * inv);
-    if (n_split > 1 && tx == 0) part_ml[row * n_split + split] = make_float2(m_run[i], l);
-  }
-}
-
 // Joins the key splits of one (token, head) row.
 template <int D>
 __global__ void __launch_bounds__(D)
@@ -535,15 +308,14 @@ int dispatch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s
   float2* part_ml =
       reinterpret_cast<float2*>(static_cast<unsigned char*>(ws) + p.po_bytes);
   const dim3 grid((unsigned)p.n_split, (unsigned)p.n_blk, (unsigned)(a.B * a.H));
-  auto go = [&](auto kern, int threads, size_t smem) -> int {
+  auto go = [&](auto kern, size_t smem) -> int {
     if (int rc = ensure_smem_attr(reinterpret_cast<const void*>(kern), (int)smem)) return rc;
-    return launch_pdl(kern, grid, dim3(threads), smem, s, a, p.n_split, part_o, part_ml);
+    return launch_pdl(kern, grid, dim3(kThreads), smem, s, a, p.n_split, part_o, part_ml);
   };
-  int rc = p.rw == 0   ? go(tree_tile_kernel<D>, kTileThreads, sizeof(TileSmem<D>))
-           : p.rw == 1 ? go(tree_simt_kernel<D, 1>, kThreads, sizeof(SimtSmem<D, 1>))
-           : p.rw == 2 ? go(tree_simt_kernel<D, 2>, kThreads, sizeof(SimtSmem<D, 2>))
-           : p.rw == 4 ? go(tree_simt_kernel<D, 4>, kThreads, sizeof(SimtSmem<D, 4>))
-                       : go(tree_simt_kernel<D, 8>, kThreads, sizeof(SimtSmem<D, 8>));
+  int rc = p.rw == 1   ? go(tree_simt_kernel<D, 1>, sizeof(SimtSmem<D, 1>))
+           : p.rw == 2 ? go(tree_simt_kernel<D, 2>, sizeof(SimtSmem<D, 2>))
+           : p.rw == 4 ? go(tree_simt_kernel<D, 4>, sizeof(SimtSmem<D, 4>))
+                       : go(tree_simt_kernel<D, 8>, sizeof(SimtSmem<D, 8>));
   if (rc || p.n_split == 1) return rc;
   return launch_pdl(tree_combine_kernel<D>, dim3((unsigned)((int64_t)a.B * a.n_max * a.Hq)),
                     dim3(D), 0, s, a, p.n_split, static_cast<const float*>(part_o),
@@ -554,18 +326,18 @@ int dispatch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s
 // row tile of 16 (with two, 17 to 32 rows, a slice took a warp so long that
 // loads waited: 16 sequences x 8,220 keys, 32 rows, 125 us against
 // tree_attn_tc.cu's 103 for 36; 64 sequences x 100 keys 46 us against 24).
-// fp32: two tiles, once there are 2e7 products of a row and a key's element in
-// the lengths that the buffers allow: its slices and merge take 11 to 14 us at
-// the least, where tree_simt_kernel takes 6 to 9 (2 sequences of 16 tokens
-// over 322 keys, 5e6 products: 12.3 against 9.0; 4 sequences x 4,104 keys, 4 /
-// 16 / 32 rows, 1.7e7 to 1.3e8: 23.6 / 26 / 36 against 23.1 / 28 / 41; 8 x
-// 32,104 keys: 143 / 147 / 273 against 218 / 448 / 742).
+// fp32: once there are 2e7 products of a row and a key's element in the lengths
+// that the buffers allow: its slices and merge take 11 to 14 us at the least,
+// where tree_simt_kernel takes 6 to 9 (2 sequences of 16 tokens over 322 keys,
+// 5e6 products: 12.3 against 9.0; 4 sequences x 4,104 keys, 4 / 16 / 32 rows,
+// 1.7e7 to 1.3e8: 23.6 / 26 / 36 against 23.1 / 28 / 41; 8 x 32,104 keys: 143 /
+// 147 / 273 against 218 / 448 / 742).
 bool takes_few(msa_dtype dt, int B, int n_max, int Hq, int H, int D, int m_cap, int max_pages,
                int page_size) {
   const int rows = n_max * (Hq / H);
   if (dt == MSA_BF16) return rows <= 16;
   const double keys = (double)m_cap + (double)max_pages * page_size;
-  return rows <= 32 && (double)rows * B * H * keys * D > 2e7;
+  return (double)rows * B * H * keys * D > 2e7;
 }
 
 // Shape checks shared by the call and its workspace size; a MSA status.

@@ -154,8 +154,8 @@ int tree_merge_launch(const TreeArgs& a, bool f32, int D, int ctas, int per, int
                       const float* part_o, const float2* part_ml, const TreeCut* cuts,
                       cudaStream_t s);
 
-// Few rows a KV head (16 in bf16, 32 in fp32): a warp a worker
-// (tree_attn_few.cu).
+// A warp a worker (tree_attn_few.cu): up to 16 rows a KV head in bf16, any
+// number in fp32.
 size_t tree_few_workspace_size(int n_max, int G, int D);
 int tree_few_launch(msa_dtype dt, const TreeArgs& a, int D, void* ws, cudaStream_t s);
 

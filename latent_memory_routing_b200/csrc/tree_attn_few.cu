@@ -1,7 +1,7 @@
 // Attention for drafted token trees over [memory ; paged cache ; drafted
 // tokens] when a KV head has few query rows (method and semantics:
-// tree_attn.cu): plain decode and small trees, R = n G <= 16 rows in bf16, 32
-// in fp32 (two items of 16).
+// tree_attn.cu): plain decode and small trees, R = n G <= 16 rows, in bf16; in
+// fp32 any number, 16 an item.
 //
 // Mathematics.  As tree_attn_tc.cu: S = Q K^T, p = 2^(scale log2(e) s - m),
 // O += p V (p in bf16 with bf16 values), l += p, one pass over the keys.
@@ -31,8 +31,13 @@
 //   * fp32 takes slices of 8 keys on m16n8k8, operands split into two tf32
 //     terms: 96 instructions a slice of 8 KB, which bound it (8 sequences x
 //     32,104 keys: 143 us, 3.7 TB/s; with a third of the products 91 us, 5.8).
+//     More rows are more items over the same keys, side by side and out of the
+//     L2: 64 tokens, 4 sequences x 4,164 keys, 8 / 2 heads, 163 us (27 TFLOP/s;
+//     fp32 register tiles of 64 x 64 one CTA a split took 169, and 648 against
+//     267 for 49 tokens over caches of up to 25,550 rows of unlike lengths).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_tc.cuh"
 #include "tc_ptx.cuh"
@@ -57,11 +62,55 @@ template <typename T, int D> struct FC {
   static constexpr size_t SMEM = 1024 + (size_t)kWarps * DEPTH * SLICE;
 };
 
-struct FewAux {
+// The drafted tokens that a row's token sees: bit t for token t, of 16 in
+// bf16, 128 in fp32.
+struct Seen16 {
+  uint32_t m;
+  __device__ __forceinline__ void clear() { m = 0; }
+  __device__ __forceinline__ void set(int t) { m |= 1u << t; }
+  __device__ __forceinline__ void upto(int t) { m = (2u << t) - 1; }
+  __device__ __forceinline__ bool any() const { return m != 0; }
+  __device__ __forceinline__ bool has(int t) const { return (m >> t) & 1; }
+  // tokens t, t + 1, .. (t may be negative: those before 0 count as seen)
+  __device__ __forceinline__ uint32_t from(int t) const {
+    return t <= -16 ? 0xffffu : t <= 0 ? (((1u << -t) - 1) | (m << -t)) : t < 32 ? m >> t : 0u;
+  }
+};
+struct Seen128 {
+  uint4 m;
+  __device__ __forceinline__ void clear() { m = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void set(int t) {
+    const uint32_t bit = 1u << (t & 31);
+    m.x |= t < 32 ? bit : 0;
+    m.y |= (t >> 5) == 1 ? bit : 0;
+    m.z |= (t >> 5) == 2 ? bit : 0;
+    m.w |= (t >> 5) == 3 ? bit : 0;
+  }
+  __device__ __forceinline__ static uint32_t word_upto(int t) {  // t within or past a word
+    return t < 0 ? 0u : t >= 31 ? 0xffffffffu : (2u << t) - 1;
+  }
+  __device__ __forceinline__ void upto(int t) {
+    m = make_uint4(word_upto(t), word_upto(t - 32), word_upto(t - 64), word_upto(t - 96));
+  }
+  __device__ __forceinline__ bool any() const { return (m.x | m.y | m.z | m.w) != 0; }
+  __device__ __forceinline__ bool has(int t) const { return tree_bit(m, t); }
+  __device__ __forceinline__ uint32_t from(int t) const {  // 16 of them at least
+    if (t <= -16) return 0xffffu;
+    if (t <= 0) return ((1u << -t) - 1) | (m.x << -t);
+    const int w = t >> 5;
+    const uint32_t lo = w == 0 ? m.x : w == 1 ? m.y : w == 2 ? m.z : w == 3 ? m.w : 0u;
+    const uint32_t hi = w == 0 ? m.y : w == 1 ? m.z : w == 2 ? m.w : 0u;
+    return __funnelshift_r(lo, hi, t & 31);
+  }
+};
+
+template <typename T> struct FewAux {
+  using Seen = std::conditional_t<sizeof(T) == 4, Seen128, Seen16>;
   int64_t pre[kFewThreads + 1];          // slices before each thread's sequences
   TreeSeq seq[kFewThreads];              // the sequences, where a thread has one at most
   uint64_t full[kWarps][6];              // ring slots (DEPTH <= 6)
-  uint32_t anc[kWarps][16];           // what each row's token sees of its tree
+  Seen seen[kWarps][16];
+  int tiles[kWarps];
   signed char par[kWarps][128];
 };
 
@@ -333,7 +382,8 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   pdl_trigger();  // the merge: its blocks come as this grid's leave
   pdl_wait();
   extern __shared__ __align__(1024) unsigned char dsm[];
-  __shared__ FewAux aux;
+  __shared__ FewAux<T> aux;
+  using Seen = typename FewAux<T>::Seen;
   unsigned char* base = tc::smem_align<1024>(dsm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* ring = base + warp * C::DEPTH * C::SLICE;
@@ -350,7 +400,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   // The slices of all sequences, a run of sequences a thread, scanned over
   // the CTA's threads.
   const int per = (a.B + kFewThreads - 1) / kFewThreads;
-  int64_t items;
+  int64_t items = 0;
   {
     int64_t mine = 0;
     int tiles = 0;
@@ -358,13 +408,11 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       const TreeSeq s = tree_seq(a, b);
       if (s.error && blockIdx.x == 0) record_error(a.status, s.error);
       aux.seq[tid] = s;
-      tiles = seq_slices<T>(s) > 0 ? row_tiles<T>(a, s) : 0;
-      mine += (int64_t)seq_slices<T>(s) * a.H * tiles;
+      if (seq_slices<T>(s) > 0) tiles += row_tiles<T>(a, s);
+      mine += (int64_t)seq_slices<T>(s) * a.H * row_tiles<T>(a, s);
     }
-    // (more sequences than threads: at least as many as there are, about)
-    items = per == 1 ? __syncthreads_count(tiles > 0) : a.B;
-    if (C::F32 && per == 1) items += __syncthreads_count(tiles > 1);
-    items *= a.H;
+    const int w_tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0) aux.tiles[warp] = w_tiles;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -378,6 +426,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) before += aux.pre[i];
       total += aux.pre[i];
+      items += (int64_t)aux.tiles[i] * a.H;
     }
     __syncthreads();
     aux.pre[tid] = before + incl - mine;
@@ -532,19 +581,20 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       }
       __syncwarp();
     }
-    if (lane < rows) {  // (a KV head's rows, so its tokens too, are 32 at most)
-      uint32_t m = 0;
+    if (lane < rows) {
+      Seen m;
+      m.clear();
       int x = (row0 + lane) / a.G;
       if (a.parents) {
         do {
-          m |= 1u << x;
+          m.set(x);
           x = aux.par[warp][x];
         } while (x >= 0);
-        if (x != -1) m = 0;  // pruned: sees nothing
+        if (x != -1) m.clear();  // pruned: sees nothing
       } else {
-        m = (2u << x) - 1;
+        m.upto(x);
       }
-      aux.anc[warp][lane] = m;
+      aux.seen[warp][lane] = m;
     }
     __syncwarp();
 
@@ -572,18 +622,11 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       float sc[C::NT][4];
       q.scores(kb_u, lane, sc);
       if (!all) {
-        const int off = s.L - key0;  // column of the first drafted key
         const uint32_t in = n_rows >= C::SL ? 0xffffu : (1u << n_rows) - 1;  // n_rows >= 1
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t vis = in;
-          if (!mem) {
-            const uint32_t anc = aux.anc[warp][r4 + 8 * h];
-            vis &= off >= 16   ? 0xffffu
-                   : off >= 0  ? (((1u << off) - 1) | (anc << off))
-                   : off > -32 ? anc >> -off
-                               : 0u;
-          }
+          if (!mem) vis &= aux.seen[warp][r4 + 8 * h].from(key0 - s.L);
 #pragma unroll
           for (int t = 0; t < C::NT; ++t)
 #pragma unroll
@@ -669,8 +712,8 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
       lr += __shfl_xor_sync(0xffffffffu, lr, 1);
       lr += __shfl_xor_sync(0xffffffffu, lr, 2);
       if (r >= rows) continue;
-      const uint32_t anc = aux.anc[warp][r];
-      if (anc == 0) lr = 0.f;  // pruned
+      const Seen seen = aux.seen[warp][r];
+      if (!seen.any()) lr = 0.f;  // pruned
       const int64_t prow = (worker * 2 + max(part, 0)) * part_rows + r;
       const float inv = lr == 0.f ? 0.f : part >= 0 ? 1.f : 1.f / lr;
       // (a row without weight: its O may hold 0 times NaN)
@@ -699,7 +742,7 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
 #pragma unroll 1
       for (int t = 0; t < s.n; ++t) {
         const int kr2 = s.L + t, j = n_ms + kr2 / C::SL;
-        if (!((anc >> t) & 1) || j < j_lo || j >= j_lo + cnt || kr2 >= s.cache) continue;
+        if (!seen.has(t) || j < j_lo || j >= j_lo + cnt || kr2 >= s.cache) continue;
         const int pg = a.block_table[(int64_t)cu.b * a.max_pages + kr2 / a.page_size];
         if (pg < 0 || pg >= a.n_pages) continue;
         const T* v = static_cast<const T*>(a.v_pages) +

@@ -157,7 +157,8 @@ template <typename T, int D>
 int launch(const TreeArgs& a, int ctas, int per, int part_rows, const float* part_o,
            const float2* part_ml, const TreeCut* cuts, cudaStream_t s) {
   const int workers = ctas * per, chunks = (workers + kChunk - 1) / kChunk;
-  const int64_t items = std::min<int64_t>(workers, (int64_t)a.B * a.H);
+  const int64_t items = std::min<int64_t>(
+      workers, (int64_t)a.B * a.H * ((a.n_max * a.G + part_rows - 1) / part_rows));
   // Few items may have many parts each: eight warps then share a row's (two
   // items of 1,256 slices and 16 rows: 50 us with a warp a row, 20).
   const bool long_items = items * 32 <= workers;
