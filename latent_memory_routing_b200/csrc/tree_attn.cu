@@ -403,9 +403,10 @@ int tree_body(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int 
   a.status = device_status_ptr();
   const TreePlan p = tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size);
   const bool few = takes_few(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size);
+  const int64_t keys = (int64_t)m_cap + (int64_t)max_pages * page_size;
   const size_t need = few               ? tree_few_workspace_size(n_max, a.G, D)
                       : dt == MSA_F32 ? p.total
-                                      : tree_tc_workspace_size(n_max, a.G, D);
+                                      : tree_tc_workspace_size(B, n_max, a.G, H, D, keys);
   if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MSA_ERR_WORKSPACE;
   if (few) return tree_few_launch(dt, a, D, ws, s);
   if (dt == MSA_BF16) return tree_tc_launch(a, D, ws, s);
@@ -421,7 +422,9 @@ extern "C" size_t msa_tree_attn_workspace_size(msa_dtype dt, int B, int n_max, i
   if (tree_shape(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size)) return 0;
   if (takes_few(dt, B, n_max, Hq, H, D, m_cap, max_pages, page_size))
     return tree_few_workspace_size(n_max, Hq / H, D);
-  if (dt == MSA_BF16) return tree_tc_workspace_size(n_max, Hq / H, D);
+  if (dt == MSA_BF16)
+    return tree_tc_workspace_size(B, n_max, Hq / H, H, D,
+                                  (int64_t)m_cap + (int64_t)max_pages * page_size);
   return tree_plan(B, n_max, Hq, H, D, m_cap, max_pages, page_size).total;
 }
 

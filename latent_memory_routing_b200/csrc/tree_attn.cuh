@@ -160,7 +160,8 @@ size_t tree_few_workspace_size(int n_max, int G, int D);
 int tree_few_launch(msa_dtype dt, const TreeArgs& a, int D, void* ws, cudaStream_t s);
 
 // bf16 on tcgen05 (tree_attn_tc.cu): any shape the entry point takes.
-size_t tree_tc_workspace_size(int n_max, int G, int D);
+// (keys: the most that the buffers allow a sequence.)
+size_t tree_tc_workspace_size(int B, int n_max, int G, int H, int D, int64_t keys);
 int tree_tc_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s);
 
 }  // namespace msa

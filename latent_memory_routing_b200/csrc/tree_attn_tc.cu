@@ -32,8 +32,11 @@
 //     in bf16), its O accumulator (D columns) and its softmax warpgroup (a
 //     thread a row).  Up to 128 rows (kQT = 1) the streams take the key tiles
 //     in turn and join their (m, l, O) at an item's end, so a stream has the
-//     time of two tiles; above (kQT = 2) each holds 128 of an item's 256 rows
-//     and both read the same tile.
+//     time of two tiles; with kQT = 2 each holds 128 of an item's 256 rows and
+//     both read the same tile.  More than 128 rows are items of their own over
+//     the same keys, out of the L2 (16 sequences x 8,220 keys, 33 tokens: 75 us
+//     against 92 with kQT = 2, 48: 108, 111), until the L2 cannot hold what two
+//     of them share (see tc_plan).
 //   * Warp 0 loads K tiles, warp 3 V tiles (rings of their own: a K slot is
 //     free after S, a V slot after P V), one lane a page (or 32 memory rows):
 //     only pages that hold rows are read.  Warp 2 walks the range, publishes
@@ -940,13 +943,18 @@ struct TcPlan {
   size_t smem, po_bytes, ml_bytes, cut_bytes, total;
 };
 
-// kQT = 2 once an item's rows exceed one MMA tile: both tiles then share one
-// pass over K and V.  The Q buffers hold no more rows than a tile can have (the
-// MMA reads on into the ring: rows of S that nobody reads).
-TcPlan tc_plan(int n_max, int G, int D) {
+// kQT = 2 where two tiles have to share one pass over K and V: more than 192
+// rows (fewer leave much of the second tile empty, and its time is spent all
+// the same) of 128 dims (at 64 the chain of a tile, not HBM, is the bound), and
+// more keys and values in the lengths that the buffers allow than the L2 keeps:
+// 64 tokens, 2 sequences x 20,064 keys (164 MB) 65 us against 71 with kQT = 1,
+// x 150,065 311 against 380; 16 x 2,064 (135 MB) 84 against 79.
+// The Q buffers hold no more rows than a tile can have (the MMA reads on into
+// the ring: rows of S that nobody reads).
+TcPlan tc_plan(int B, int n_max, int G, int H, int D, int64_t keys) {
   TcPlan p{};
   const int rows = n_max * G;
-  p.qt = rows > 128 ? 2 : 1;
+  p.qt = rows > 192 && D == 128 && (double)B * H * keys * D * 4 > 150e6 ? 2 : 1;
   p.tile_tok = std::min(n_max, 128 / G);
   p.part_rows = std::min(rows, p.tile_tok * G * p.qt);
   p.q_rows = (p.tile_tok * G + 7) / 8 * 8;
@@ -987,11 +995,14 @@ int launch_tc(const TreeArgs& a, const TcPlan& p, void* ws, cudaStream_t s) {
 
 }  // namespace
 
-size_t tree_tc_workspace_size(int n_max, int G, int D) { return tc_plan(n_max, G, D).total; }
+size_t tree_tc_workspace_size(int B, int n_max, int G, int H, int D, int64_t keys) {
+  return tc_plan(B, n_max, G, H, D, keys).total;
+}
 
 int tree_tc_launch(const TreeArgs& a, int D, void* ws, cudaStream_t s) {
-  const TcPlan p = tc_plan(a.n_max, a.G, D);
-  if (D == 64) return p.qt == 1 ? launch_tc<64, 1>(a, p, ws, s) : launch_tc<64, 2>(a, p, ws, s);
+  const TcPlan p = tc_plan(a.B, a.n_max, a.G, a.H, D,
+                           (int64_t)a.m_cap + (int64_t)a.max_pages * a.page_size);
+  if (D == 64) return launch_tc<64, 1>(a, p, ws, s);
   return p.qt == 1 ? launch_tc<128, 1>(a, p, ws, s) : launch_tc<128, 2>(a, p, ws, s);
 }
 

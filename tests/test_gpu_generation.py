@@ -462,6 +462,20 @@ def test_few_rows_over_short_and_long_items(lens, toks, H):
     status()
 
 
+@pytest.mark.parametrize("page,Hq,H,lens,toks,mem,tree,n_max", [
+    (64, 8, 2, [18500] + [300, 0, 129] * 4, [64, 33, 1, 20] * 3 + [64], [], "tree", 64),
+    (16, 14, 2, [9400, 12] * 10, [32, 31] * 10, [100, 0] * 10, "pruned", 32),
+    (128, 16, 1, [70000, 0, 250, 2, 1], [128, 128, 17, 5, 0], [], "chain", 128)])
+def test_two_query_tiles_share_a_pass(page, Hq, H, lens, toks, mem, tree, n_max):
+    """More than 192 rows a KV head and room for more keys than the L2 keeps,
+    most of it unused."""
+    t = tree_case(BF16, page, Hq, H, 128, lens, toks, mem, tree, seed=19, lead=2)
+    out = run_tree(t, n_max)
+    check_tree(t, out)
+    assert torch.equal(out.view(torch.int16), run_tree(t, n_max).view(torch.int16))
+    status()
+
+
 @pytest.mark.parametrize("page,Hq,H,D,lens,toks,mem,tree,n_max", [
     (16, 4, 2, 64, [6100, 0, 17], [16, 1, 5], [6, 0, 3], "tree", 16),
     (32, 3, 3, 128, [40000, 31], [1, 1], [], "chain", 1),
@@ -505,7 +519,8 @@ def test_padding_tokens_are_left_alone_and_scale_is_used(dt):
 
 @pytest.mark.parametrize("dt,D,n,rows", [(F32, 64, 12, 45), (F32, 64, 20, 45), (F32, 64, 8, 12005),
                                          (F32, 64, 16, 7001), (BF16, 64, 8, 45),
-                                         (BF16, 64, 20, 45), (BF16, 128, 100, 45)])
+                                         (BF16, 64, 20, 45), (BF16, 128, 100, 45),
+                                         (BF16, 128, 100, 150001)])
 def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n, rows):
     """A drafted token's NaN or infinite K and V reach the rows that see it
     and no others."""
