@@ -14,16 +14,17 @@
 // cores and the exponentials.  So the same tile shape serves all R: rows
 // padded to the MMA's M = 128 cost tensor time that the stream hides.
 // Measured (32 / 8 heads x 128): 16 sequences x 8,220 keys, 9 to 32 tokens
-// each, 103 to 116 us (5.3 to 4.7 TB/s); 64 tokens, 173 us; 2 x 150,001 keys,
-// 64 tokens, 350 us (0.9 PFLOP/s: the chain softmax -> P V -> S of each
-// stream, 3,650 cycles a tile of which the tensor pipe works 2,048).
+// each, 103 to 116 us (5.3 to 4.7 TB/s); 2 x 150,001 keys, 64 tokens, 320 to
+// 375 us as the clock goes (0.84 to 0.98 PFLOP/s: the chain softmax -> P V -> S
+// of each stream, 3,650 cycles a tile of which the tensor pipe works 2,048).
 //
 // Design.
 //   * Even work: the 128-key tiles of all (sequence, KV head, row block)
 //     items in one line, each item's behind kItemCost units that stand for its
-//     start and end (about 12,000 cycles, 3 tiles' time: without them a CTA of
-//     short items ended at 248,000 cycles, the others at 145,000), cut into
-//     one contiguous range a CTA (one CTA an SM).
+//     start and end (without them a CTA of short items ended at 248,000
+//     cycles, the others at 145,000; 16 sequences x 8,220 keys, up to 48
+//     tokens: 124 us with 1, 108 with 3, 103 with 5, 102 with 8), cut into one
+//     contiguous range a CTA (one CTA an SM).
 //     An item inside one range is written directly; an item cut by a range
 //     border is written as fp32 partials (at most two a CTA) that a second
 //     launch merges in a fixed order.  The lengths stay on the device: every
@@ -35,7 +36,7 @@
 //     time of two tiles; with kQT = 2 each holds 128 of an item's 256 rows and
 //     both read the same tile.  More than 128 rows are items of their own over
 //     the same keys, out of the L2 (16 sequences x 8,220 keys, 33 tokens: 75 us
-//     against 92 with kQT = 2, 48: 108, 111), until the L2 cannot hold what two
+//     against 92 with kQT = 2), until the L2 cannot hold what two
 //     of them share (see tc_plan).
 //   * Warp 0 loads K tiles, warp 3 V tiles (rings of their own: a K slot is
 //     free after S, a V slot after P V), one lane a page (or 32 memory rows):
@@ -65,7 +66,7 @@ constexpr int kRing = 64 * 1024; // the K ring, and the V ring
 constexpr int kStage = 4096;    // an output buffer of each softmax warp
 constexpr int kSched = 3;       // published items
 constexpr int kReaders = 11;    // K warp, V warp, MMA, 8 softmax warps
-constexpr int kItemCost = 3;    // what an item's start and end cost, in tiles
+constexpr int kItemCost = 5;    // what an item's start and end cost, in tiles
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D> struct TC {
