@@ -31,7 +31,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int workers, int most, int
                   const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                   const TreeCut* __restrict__ cuts) {
   constexpr int VEC = D / 32;
-  constexpr int kBatch = kCtas == 1 ? 8 : 5;  // partial rows a warp has in flight
+  constexpr int kBatch = kCtas == 1 ? 8 : 3;  // partial rows a warp has in flight
   __shared__ __align__(16) float so[kMergeWarps][D];
   __shared__ float2 sml[kMergeWarps];
   pdl_trigger();
