@@ -452,13 +452,30 @@ def test_many_short_sequences(dt, Hq, n):
     status()
 
 
-@pytest.mark.parametrize("lens,toks,H", [([3] * 33, [6] * 33, 2), ([1, 0, 90, 7, 33, 5], [3] * 6, 4),
-                                         ([130], [2], 1), ([2000], [1], 1), ([4100, 5], [1, 4], 2),
-                                         ([20000], [1], 1)])
+@pytest.mark.parametrize("lens,toks,H", [
+    ([3] * 33, [6] * 33, 2), ([1, 0, 90, 7, 33, 5], [3] * 6, 4), ([130], [2], 1),
+    ([2000], [1], 1), ([4100, 5], [1, 4], 2), ([20000], [1], 1)])
 def test_few_rows_over_short_and_long_items(lens, toks, H):
     """Items kept whole, and cut into ranges of one slice and of more."""
     t = tree_case(BF16, 16, 2 * H, H, 64, lens, toks, [], "chain", seed=3)
     check_tree(t, run_tree(t, max(toks)))
+    status()
+
+
+@pytest.mark.parametrize("dt,Hq,H,D,lens,toks,mem,tree,n_max", [
+    (F32, 16, 1, 64, [(i * 37) % 211 for i in range(300)], [i % 9 for i in range(300)], [], "tree",
+     8),
+    (F32, 16, 1, 64, [700, 0], [128, 77], [3, 0], "pruned", 128),
+    (F32, 16, 4, 128, [0] * 8, [64] * 8, [], "chain", 64),
+    (F32, 16, 8, 128, [3000] * 4, [0] * 4, [], "chain", 16),
+    (F32, 4, 1, 64, [9000] + [1] * 60, [3] + [4] * 60, [0] * 60 + [50], "roots", 4),
+    (BF16, 16, 4, 128, [9000] + [1] * 60, [3] + [4] * 60, [0] * 60 + [50], "roots", 4),
+    (BF16, 16, 4, 128, [9000] + [1] * 60, [33] + [4] * 60, [0] * 60 + [50], "tree", 48),
+    (BF16, 2, 1, 64, [4, 0], [0, 0], [], "chain", 1),
+    (BF16, 1, 1, 64, [i % 3 for i in range(1000)], [i % 2 for i in range(1000)], [], "chain", 1)])
+def test_unlike_and_empty_sequences(dt, Hq, H, D, lens, toks, mem, tree, n_max):
+    t = tree_case(dt, 16, Hq, H, D, lens, toks, mem, tree, seed=1, lead=2)
+    check_tree(t, run_tree(t, n_max))
     status()
 
 
