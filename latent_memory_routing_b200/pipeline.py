@@ -413,7 +413,10 @@ class PagedCache:
     ``page_size`` rows: the pools k_pages, v_pages [n_pages][H][page_size][D],
     the sequences' page lists block_table [B][max_pages] and their lengths
     cache_len [B] (int32, device).  Pages are handed out on the host
-    (``reserve``, ``release``); rows are written by ``append``."""
+    (``reserve``, ``release``); rows are written by ``append``.  Entries of the
+    block table without a page hold -1, which the kernels refuse: a token
+    appended past the reserved rows, or to a released sequence, is recorded in
+    the device status word and written nowhere."""
 
     def __init__(self, dtype, n_pages: int, page_size: int, H: int, D: int, B: int,
                  max_pages: int, device):
@@ -421,7 +424,7 @@ class PagedCache:
         self.B, self.H, self.D = B, H, D
         self.k_pages = torch.empty((n_pages, H, page_size, D), dtype=dtype, device=device)
         self.v_pages = torch.empty_like(self.k_pages)
-        self.block_table = torch.zeros((B, max_pages), dtype=torch.int32, device=device)
+        self.block_table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
         self.cache_len = torch.zeros(B, dtype=torch.int32, device=device)
         self.free = list(range(n_pages - 1, -1, -1))
         self.owned = [[] for _ in range(B)]
@@ -443,6 +446,7 @@ class PagedCache:
         """Takes sequence b's pages back and empties it."""
         self.free += reversed(self.owned[b])
         self.owned[b] = []
+        self.block_table[b] = -1  # its pages may soon be another sequence's
         self.cache_len[b] = 0
 
     def append(self, k, v, tok_offsets, positions, k_weight=None, q=None, q_weight=None,

@@ -261,3 +261,15 @@ def test_paged_cache_hands_out_and_takes_back_pages():
     c.reserve(0, 1)
     assert c.block_table[0, 0].item() == 0
     assert sorted(c.owned[0] + c.owned[1] + c.free) == list(range(5))
+
+
+def test_paged_cache_names_no_page_that_a_sequence_does_not_own():
+    """Entries without a page are -1, from the start and after a release."""
+    c = pipeline.PagedCache(torch.float32, 5, 16, 1, 64, 2, 3, "cpu")
+    assert bool((c.block_table == -1).all())
+    c.reserve(0, 17)
+    assert c.block_table.tolist() == [[0, 1, -1], [-1, -1, -1]]
+    c.release(0)
+    assert bool((c.block_table == -1).all())
+    c.reserve(1, 33)                      # the released pages are sequence 1's now
+    assert c.block_table[0].tolist() == [-1] * 3 and c.owned[1] == [0, 1, 2]

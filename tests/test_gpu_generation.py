@@ -321,6 +321,35 @@ def test_append_skips_rows_it_cannot_place(what, code):
     assert written == 2 + {"page": 1, "minus": 1, "length": 2, "full": 1}[what]
 
 
+@pytest.mark.parametrize("case", ["past_the_reserved", "never_reserved", "released"])
+def test_append_without_a_page_leaves_the_other_sequences_alone(case):
+    """The rows of sequence 0, some of them on pages that sequence 1 had."""
+    c = pipeline.PagedCache(F32, 6, 16, 2, 64, 2, 3, "cuda")
+    c.k_pages.fill_(NAN)
+    c.v_pages.fill_(NAN)
+    if case == "released":
+        c.reserve(1, 40)
+        c.release(1)
+    elif case == "past_the_reserved":
+        c.reserve(1, 16)
+    c.reserve(0, 48)
+    k, v = rnd((48, 2, 64), F32, 1), rnd((48, 2, 64), F32, 2)
+    c.append(k, v, i64([0, 48, 48]), i32(np.arange(48)))
+    status()
+    c.cache_len.copy_(i32([48, 15 if case == "past_the_reserved" else 0]))
+    before = [p.clone() for p in (c.k_pages, c.v_pages)]
+    new = rnd((3, 2, 64), F32, 3)
+    c.append(new, new, i64([0, 0, 3]), i32(np.arange(3)))
+    status(-1)
+    if case == "past_the_reserved":       # its one row with a place
+        pg = c.owned[1][0]
+        assert torch.equal(c.v_pages[pg, :, 15], new[0])
+        for p, b in zip((c.k_pages, c.v_pages), before):
+            p[pg, :, 15] = b[pg, :, 15]
+    assert all(torch.equal(p.view(torch.int32), b.view(torch.int32))
+               for p, b in zip((c.k_pages, c.v_pages), before))
+
+
 def test_two_tokens_of_a_sequence_cross_a_page():
     c = paged(1, 1, 64, BF16, 16, [48], 9)
     c.cache_len.fill_(15)
