@@ -4,13 +4,17 @@
 // fp32 any number, 16 an item.
 //
 // Mathematics.  As tree_attn_tc.cu: S = Q K^T, p = 2^(scale log2(e) s - m),
-// O += p V (p in bf16 with bf16 values), l += p, one pass over the keys.
+// O += p V, l += p, one pass over the keys.  With bf16 values p is two bf16
+// terms, p = hi + lo to 2^-16 of it: one term alone moved an output by up to
+// 2^-8 of sum p |v|, more than its own rounding (relative error over an output
+// 0.0023, with two 0.0017), and the second costs 2% (64 sequences x 2,268 keys:
+// 103 us with one, 105 with two).
 //
 // What bounds it.  4 D bytes a key and KV head against 4 R D operations: HBM,
 // by far, so all that matters is bytes in flight and what happens at the ends
 // of short sequences.  A 128-row tensor-core tile would spend most of its
 // latency on handshakes for rows that do not exist (64 sequences x 2,268 keys,
-// one token each: 114 us in tree_attn_tc.cu, 103 here with the merge, 5.8
+// one token each: 114 us in tree_attn_tc.cu, 105 here with the merge, 5.7
 // TB/s); here every warp is a worker of its own:
 //   * The 16-key slices of all (sequence, KV head) items stand in one line,
 //     cut into one contiguous range a worker (neighbours on different SMs).
@@ -22,8 +26,8 @@
 //     on its own barriers, and no warp waits for another.
 //   * A slice is 16 x 16 of S and 16 x D of O on the warp-level
 //     tensor instructions (m16n8k16): the accumulators stay in registers and
-//     P's fragment is S's.  Their rate is no limit: a slice's 64 instructions
-//     against the 8 KB that its SM receives in 350 cycles.
+//     P's fragment is S's.  Their rate is hardly a limit: a slice's 48
+//     instructions against the 8 KB that its SM receives in 350 cycles.
 //   * In a slice that reaches past the sequence's rows or into its drafted
 //     rows, unseen scores become -inf, V rows past the end zero, and
 //     non-finite drafted values are taken out of V (0 times them would reach
@@ -123,6 +127,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+// What pack2(a, b) = h left of a and b, in bf16 too.
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t h) {
+  return pack2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -216,12 +224,16 @@ template <int D> struct Rows<__nv_bfloat16, D> {
     const int vr = (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
     const uint32_t pf[4] = {pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]),
                             pack2(p[1][0], p[1][1]), pack2(p[1][2], p[1][3])};
+    const uint32_t pr[4] = {rest2(p[0][0], p[0][1], pf[0]), rest2(p[0][2], p[0][3], pf[1]),
+                            rest2(p[1][0], p[1][1], pf[2]), rest2(p[1][2], p[1][3], pf[3])};
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       uint32_t b[4];
       ldsm4t(vb_u + (d >> 2) * C::BLK + vr * 128 + (((2 * (d & 3) + vc) ^ (vr & 7)) << 4), b);
       mma16(o[2 * d], pf, b[0], b[1]);
       mma16(o[2 * d + 1], pf, b[2], b[3]);
+      mma16(o[2 * d], pr, b[0], b[1]);
+      mma16(o[2 * d + 1], pr, b[2], b[3]);
     }
   }
   __device__ __forceinline__ static int col(int d, int x, int lane) {

@@ -538,6 +538,27 @@ def test_long_fp32_items(page, Hq, H, D, lens, toks, mem, tree, n_max):
     status()
 
 
+@pytest.mark.parametrize("Hq,H,D,lens,toks,mem,tree", [
+    (32, 8, 128, [2047, 5, 0, 640], [1] * 4, [220, 0, 1, 16], "chain"),
+    (8, 2, 64, [4000, 9], [4, 3], [], "tree"),
+    (16, 1, 128, [9000], [1], [33], "chain")])
+def test_few_rows_in_bf16_round_once(Hq, H, D, lens, toks, mem, tree):
+    """Up to 16 rows a KV head: an output is rounded to bf16 (BF of itself) and
+    what is behind it is exact to the fp32 terms of `expected` and to the two
+    bf16 terms of a weight (each leaves at most BF of what it is to hold)."""
+    t = tree_case(BF16, 16, Hq, H, D, lens, toks, mem, tree, seed=12)
+    out = run_tree(t, max(toks))
+    want, tol = expected(t)
+    c, q, off, parents, km, vm, ml, _ = t
+    _, bound, _ = oracle.tree_attn(
+        f64(q), off.cpu().numpy(), None if parents is None else parents.cpu().numpy(), f64(km),
+        f64(vm), None if ml is None else ml.cpu().numpy(), f64(c.k_pages), f64(c.v_pages),
+        c.block_table.cpu().numpy(), c.cache_len.cpu().numpy())
+    behind = tol - BF * bound - BF * np.abs(want) + BF * BF * bound
+    close(out, want, behind * (1 + BF) + BF * np.abs(want))
+    status()
+
+
 @pytest.mark.parametrize("n_max", [1, 4, 5, 8, 9, 32, 33, 100, 128])
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_row_counts_around_the_kernels_tiles(dt, n_max):
