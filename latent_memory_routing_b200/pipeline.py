@@ -322,9 +322,9 @@ class Pipeline:
 
 
 def _made(stream, make):
-    """make() with its tensors belonging to the stream the call runs on (an
-    int is a raw handle), so that their memory is not handed on while it
-    runs."""
+    """make() on the stream the call runs on (an int is a raw handle): the
+    tensors made belong to it, so that their memory is not handed on while it
+    runs, and what is written is in order with it."""
     if stream is None:
         return make()
     if isinstance(stream, int):
@@ -416,7 +416,9 @@ class PagedCache:
     (``reserve``, ``release``); rows are written by ``append``.  Entries of the
     block table without a page hold -1, which the kernels refuse: a token
     appended past the reserved rows, or to a released sequence, is recorded in
-    the device status word and written nowhere."""
+    the device status word and written nowhere.  ``reserve`` and ``release``
+    write the table and the lengths on ``stream`` (the current one if None):
+    the one the cache's calls run on, or one ordered with it."""
 
     def __init__(self, dtype, n_pages: int, page_size: int, H: int, D: int, B: int,
                  max_pages: int, device):
@@ -429,7 +431,7 @@ class PagedCache:
         self.free = list(range(n_pages - 1, -1, -1))
         self.owned = [[] for _ in range(B)]
 
-    def reserve(self, b: int, rows: int):
+    def reserve(self, b: int, rows: int, stream=None):
         """Gives sequence b pages for at least ``rows`` rows in all."""
         have = len(self.owned[b])
         need = -(-rows // self.page_size) - have
@@ -439,15 +441,23 @@ class PagedCache:
             raise _m.MsaError("PagedCache.reserve", -3, f"sequence {b}, {rows} rows")
         new = [self.free.pop() for _ in range(need)]
         self.owned[b] += new
-        self.block_table[b, have:have + need] = torch.tensor(
-            new, dtype=torch.int32, device=self.block_table.device)
 
-    def release(self, b: int):
+        def write():
+            self.block_table[b, have:have + need] = torch.tensor(
+                new, dtype=torch.int32, device=self.block_table.device)
+
+        _made(stream, write)
+
+    def release(self, b: int, stream=None):
         """Takes sequence b's pages back and empties it."""
         self.free += reversed(self.owned[b])
         self.owned[b] = []
-        self.block_table[b] = -1  # its pages may soon be another sequence's
-        self.cache_len[b] = 0
+
+        def write():
+            self.block_table[b] = -1  # its pages may soon be another sequence's
+            self.cache_len[b] = 0
+
+        _made(stream, write)
 
     def append(self, k, v, tok_offsets, positions, k_weight=None, q=None, q_weight=None,
                eps: float = 1e-6, rope_base: float = 10000.0, q_out=None, stream=None):

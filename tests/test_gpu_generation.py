@@ -884,6 +884,33 @@ def test_calls_on_two_streams_at_once():
     status()
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_pages_are_handed_over_on_the_calls_stream(raw):
+    """Reservations, appends and releases on a stream of their own, while the
+    current stream is busy: the next append sees the pages of the last reserve."""
+    s = torch.cuda.Stream()
+    st = s.cuda_stream if raw else s
+    c = pipeline.PagedCache(F32, 4, 16, 2, 64, 2, 2, "cuda")
+    c.v_pages.fill_(NAN)
+    k, off, pos = rnd((16, 2, 64), F32, 1), i64([0, 16, 16]), i32(np.arange(16))
+    other = i64([0, 0, 16])
+    busy = rnd((4096, 4096), F32, 2)
+    torch.cuda.synchronize()
+    for i in range(6):
+        for _ in range(8):
+            busy = busy @ busy * 1e-3
+        b = i & 1
+        c.reserve(b, 16, stream=st)
+        c.append(k, k, other if b else off, pos, stream=st)
+        if i < 5:
+            c.release(b, stream=st)
+    s.synchronize()
+    assert torch.equal(c.v_pages[c.owned[1][0]].transpose(0, 1), k)
+    torch.cuda.synchronize()
+    assert c.block_table.tolist() == [[-1, -1], [c.owned[1][0], -1]]
+    status()
+
+
 def test_a_backward_call_on_another_stream():
     n, Hq, H, D = 4000, 8, 2, 128
     _, q, k, wq, wk, pos = norm_inputs(BF16, n, Hq, H, D, "qk", "near", seed=1)
