@@ -18,7 +18,7 @@
 // to come into its own slots of shared memory (cp.async), kDepth passes
 // ahead, with no barrier between lanes and no registers held (loads straight
 // into registers reached 4.1 TB/s with one pass a warp in flight and 5.1 with
-// five; this 5.9, the gradient 5.8, a plain copy 6.6).  A token's D / 2
+// five; this 6.2, the gradient 5.8, a plain copy 6.6).  A token's D / 2
 // (cos, sin) are built once, two or fewer a lane, for all its rows.  Tokens
 // of few rows leave lanes of a pass empty, and the instructions of a pass
 // bound them instead: 123,000 tokens of 8 + 1 heads of 64, 2.6 TB/s.
@@ -327,7 +327,7 @@ norm_rope_kernel(const __grid_constant__ NRArgs a) {
 
   stage_weight<T, D>(a.wq, wts[0]);
   stage_weight<T, D>(a.wk, wts[1]);
-  if (!rot)
+  if (!rot)  // (the sines are not used)
     for (int i = lane; i < D; i += 32) cs[i] = i < HALF ? 1.f : 0.f;
   __syncthreads();
   uint64_t freq[HALF / 32];
@@ -454,11 +454,19 @@ norm_rope_kernel(const __grid_constant__ NRArgs a) {
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (kAppend || rot) {
 #pragma unroll
-        for (int e = 0; e < NP2; ++e) {
-          const f2 y1 = fma2(x1[u][e], ca[e], mul2(x2[u][e], cb[e]));
-          x2[u][e] = fma2(x2[u][e], cc[e], mul2(x1[u][e], cd[e]));
-          x1[u][e] = y1;
+          for (int e = 0; e < NP2; ++e) {
+            const f2 y1 = fma2(x1[u][e], ca[e], mul2(x2[u][e], cb[e]));
+            x2[u][e] = fma2(x2[u][e], cc[e], mul2(x1[u][e], cd[e]));
+            x1[u][e] = y1;
+          }
+        } else {  // (0 times an infinite partner would be NaN)
+#pragma unroll
+          for (int e = 0; e < NP2; ++e) {
+            x1[u][e] = mul2(x1[u][e], ca[e]);
+            x2[u][e] = mul2(x2[u][e], cc[e]);
+          }
         }
         r1[u] = from_pairs<T>(x1[u]);
         r2[u] = from_pairs<T>(x2[u]);

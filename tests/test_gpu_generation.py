@@ -135,6 +135,35 @@ def test_norm_rope(case):
     status()
 
 
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_infinite_element_stays_where_it_is_without_positions(dt, D):
+    """r = 0 makes it NaN and the others 0; in a tensor that is neither normed
+    nor rotated nothing changes."""
+    q, k = rnd((7, 3, D), dt, 1), rnd((7, 2, D), dt, 2)
+    at = [(0, 0, 0), (3, 2, D // 2), (6, 1, D - 1), (5, 0, 5)]
+    for i, (t, h, d) in enumerate(at):
+        q[t, h, d] = float("inf") * (-1) ** i
+    k[4, 1, 9] = float("inf")
+    w = rnd((D,), dt, 3) * 0.2 + 1
+    yq, yk = pipeline.qk_norm_rope(q, k, None, w, None)
+    assert torch.equal(yk, k)
+    with np.errstate(invalid="ignore"):
+        want = oracle.norm_rope(f64(q), f64(w), None)
+    assert np.isnan(want).sum() == len(at)
+    assert np.array_equal(np.isnan(f64(yq)), np.isnan(want))
+    for t, h, _ in at:
+        assert bool((yq[t, h] == 0).sum() == D - 1)
+    # the gradient of such a row: as the formula's, element by element
+    dy = rnd((7, 3, D), dt, 4)
+    dq = pipeline.qk_norm_rope_backward(q, None, None, dy, None, w)[0]
+    rows = torch.zeros((7, 3), dtype=torch.bool, device="cuda")
+    for t, h, _ in at:
+        rows[t, h] = True
+    assert not bool(dq[~rows].isnan().any())
+    status()
+
+
 def test_norm_rope_in_place_is_the_same_bits():
     q, k = rnd((77, 6, 64), BF16, 1), rnd((77, 2, 64), BF16, 2)
     w, pos = rnd((64,), BF16, 3), i32(np.arange(77))
