@@ -69,6 +69,11 @@ constexpr int kTcThreads = 384; // 4 single warps, 2 softmax warpgroups
 constexpr int kRing = 64 * 1024; // the K ring, and the V ring
 constexpr int kStage = 4096;    // an output buffer of each softmax warp
 constexpr int kSched = 3;       // published items
+// Items whose `bad` is kept: one more than are published.  With items of one
+// tile (kQT = 1) a stream may clean V for item k + 3, whose slot is free once
+// everyone has read item k, while a warp of the other stream has yet to look at
+// bad of item k; item k + 4 is that stream's own.
+constexpr int kBad = kSched + 1;
 constexpr int kReaders = 11;    // K warp, V warp, MMA, 8 softmax warps
 constexpr int kItemCost = 5;    // what an item's start and end cost, in tiles
 constexpr float kRescaleLog2 = 8.f;
@@ -98,7 +103,7 @@ struct Aux {
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], o_empty[2], ml_full;
   uint64_t sched_full[kSched], par_full[kSched], sched_empty[kSched];
   ItemE item[kSched];
-  int bad[kSched];             // item ordinal + 1 where V held non-finite drafted values
+  int bad[kBad];               // item ordinal + 1 where V held non-finite drafted values
   float2 ml[128];              // (m, l) of the stream that does not finish the item
   signed char par[kSched][128];  // the published items' parents: -1 root, -2 pruned
   int64_t start;               // first tile of the range within its sequence
@@ -198,8 +203,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       tc::mbar_init(&aux.sched_full[i], 1);
       tc::mbar_init(&aux.par_full[i], 1);
       tc::mbar_init(&aux.sched_empty[i], kReaders);
-      aux.bad[i] = 0;
     }
+    for (int i = 0; i < kBad; ++i) aux.bad[i] = 0;
     aux.abort_flag = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tm_kp);
@@ -702,7 +707,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
               }
               *v = x;
             }
-            if (bad) *(volatile int*)&aux.bad[k % kSched] = (int)k + 1;
+            if (bad) *(volatile int*)&aux.bad[k % kBad] = (int)k + 1;
             tc::fence_proxy_async_smem();
           }
           if (warp_on) {
@@ -817,7 +822,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             m_run = m;
           }
           tc::tc_fence_after();
-          const bool bad = *(volatile int*)&aux.bad[k % kSched] == (int)k + 1;
+          const bool bad = *(volatile int*)&aux.bad[k % kBad] == (int)k + 1;
           if (e.part < 0) {
             const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
             c0 *= inv;

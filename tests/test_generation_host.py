@@ -273,3 +273,62 @@ def test_paged_cache_names_no_page_that_a_sequence_does_not_own():
     assert bool((c.block_table == -1).all())
     c.reserve(1, 33)                      # the released pages are sequence 1's now
     assert c.block_table[0].tolist() == [-1] * 3 and c.owned[1] == [0, 1, 2]
+
+
+# ------------------------------------------------- the tcgen05 kernel's flags
+
+def _flag_overwritten(n_flags, n_sched, items=9, warps=2):
+    """Whether some order of the tcgen05 tree attention's steps lets an item
+    write its flag, bad[item % n_flags], before a warp has read that of an
+    earlier item.  The roles are those of csrc/tree_attn_tc.cu with one query
+    tile and items of one key tile: the MMA thread issues S(v) once the item is
+    published and P V(v - 2) has been issued, P V(v) once every warp of stream
+    v & 1 has written P(v) and left O(v - 2); a warp takes note of every item,
+    and of its stream's own writes the flag between S and P and reads it after
+    P V.  All orders are tried."""
+    start = (((0, 0),) * (2 * warps), 0, 0)  # (item, step) of a warp; S, P V issued
+    seen, todo = {start}, [start]
+    while todo:
+        ws, vs, vp = todo.pop()
+        of = [i // warps for i in range(2 * warps)]
+
+        def past(k, step, stream=None):
+            return all(w >= (k, step) for i, w in enumerate(ws) if stream in (None, of[i]))
+
+        def published(k):
+            return k < n_sched or (past(k - n_sched, 1) and vp > k - n_sched)
+
+        after = []
+        if vs < min(items, vp + 2) and published(vs):
+            after.append((ws, vs + 1, vp))
+        if vp < vs and past(vp, 2, vp & 1) and (vp < 2 or past(vp - 1, 0, vp & 1)):
+            after.append((ws, vs, vp + 1))
+        for i, (k, step) in enumerate(ws):
+            to = None
+            if k < items and step == 0 and published(k):
+                to = (k, 1) if k & 1 == of[i] else (k + 1, 0)
+            elif step == 1 and vs > k:
+                if any(j & 1 == of[x] and j < k and j % n_flags == k % n_flags and s > 0
+                       for x, (j, s) in enumerate(ws)):
+                    return True
+                to = (k, 2)
+            elif step == 2 and vp > k:
+                to = (k + 1, 0)
+            if to:
+                after.append((ws[:i] + (to,) + ws[i + 1:], vs, vp))
+        todo += [a for a in after if a not in seen]
+        seen.update(after)
+    return False
+
+
+def test_tree_attention_flags_outlive_their_readers():
+    import os
+    import re
+    path = os.path.join(msa.PKG, "csrc", "tree_attn_tc.cu")
+    with open(path, encoding="utf-8") as f:
+        text = f.read()
+    n_sched = int(re.search(r"constexpr int kSched = (\d+);", text).group(1))
+    extra = int(re.search(r"constexpr int kBad = kSched \+ (\d+);", text).group(1))
+    assert "int bad[kBad];" in text and text.count("aux.bad[k % kBad]") == 2
+    assert _flag_overwritten(n_sched, n_sched)
+    assert not _flag_overwritten(n_sched + extra, n_sched)
