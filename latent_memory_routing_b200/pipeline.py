@@ -498,6 +498,13 @@ class TreeAttention:
                              f"the attention was made for {B} x {H} x {D}")
         if q.shape[1:] != (Hq, D):
             raise ValueError(f"q has shape {tuple(q.shape)}, needs [n, {Hq}, {D}]")
+        for what, t in (("k_mem", k_mem), ("v_mem", v_mem)):
+            # rows of another capacity would be read from the wrong places, or
+            # (m_cap = 0) left out
+            have = None if t is None or isinstance(t, int) else tuple(t.shape)
+            if (m_cap > 0 if t is None else have not in (None, (B, m_cap, H, D))):
+                raise ValueError(f"{what} has shape {have}, the attention was made for "
+                                 f"[{B}, {m_cap}, {H}, {D}]")
         if out is None:
             out = _made(stream, lambda: _dense(q))
         _m.msa_tree_attn(self.dt, B, q.shape[0], n_max, Hq, H, D, q, tok_offsets, parents, k_mem,

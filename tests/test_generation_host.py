@@ -241,6 +241,27 @@ def test_binding_refuses_a_cache_of_other_sizes(stub):
     assert [n for n, _ in stub.calls] == ["msa_paged_append", "msa_tree_attn_workspace_size"]
 
 
+def test_attention_refuses_memory_of_other_sizes(stub):
+    """Read as [B][m_cap] rows, or left out with m_cap = 0, it would answer for
+    another memory."""
+    c = pipeline.PagedCache(torch.float32, 4, 16, 2, 64, 2, 3, "cpu")
+    q, off = torch.zeros(5, 4, 64), torch.zeros(3, dtype=torch.int64)
+    ml = torch.zeros(2, dtype=torch.int32)
+    rows = {m: torch.zeros(2, m, 2, 64) for m in (0, 6, 7)}
+    none, six = (pipeline.TreeAttention(torch.float32, 2, 4, 4, 2, 64, m, 3, 16, "cpu")
+                 for m in (0, 6))
+    stub.calls.clear()
+    none(q, off, c)
+    none(q, off, c, k_mem=rows[0], v_mem=rows[0], mem_len=ml)
+    six(q, off, c, k_mem=rows[6], v_mem=rows[6], mem_len=ml)
+    assert len(stub.calls) == 3
+    for att, k, v, what in ((none, 6, 6, "k_mem"), (six, 7, 7, "k_mem"), (six, None, 6, "k_mem"),
+                            (six, 6, 0, "v_mem"), (six, 6, 7, "v_mem"), (six, 6, None, "v_mem")):
+        with pytest.raises(ValueError, match=f"{what} has shape"):
+            att(q, off, c, k_mem=rows.get(k), v_mem=rows.get(v), mem_len=ml)
+    assert len(stub.calls) == 3
+
+
 # --------------------------------------------------------------- page lists
 
 def test_paged_cache_hands_out_and_takes_back_pages():
