@@ -467,7 +467,7 @@ class PagedCache:
         queries ``q`` [N][Hq][D], norms and rotates them in the same launch
         and returns them (``q_out``, made here if None)."""
         n = k.shape[0]
-        _same_tokens(n, self.D, q=q)
+        _same_tokens(n, self.D, v=v, q=q)
         if q is not None and q_out is None:
             q_out = _made(stream, lambda: _dense(q))
         _m.msa_paged_append(dt_code(k), self.B, n, _heads(q), self.H, self.D, q, k, v, q_weight,

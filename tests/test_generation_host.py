@@ -224,6 +224,15 @@ def test_binding_refuses_operands_of_different_lengths(stub):
     assert [n for n, _ in stub.calls] == ["msa_tree_attn_workspace_size"]
 
 
+def test_append_refuses_values_of_more_tokens_than_keys(stub):
+    """Their rows would be written nowhere."""
+    c = pipeline.PagedCache(torch.float32, 4, 16, 2, 64, 2, 3, "cpu")
+    off, pos = torch.zeros(3, dtype=torch.int64), torch.zeros(6, dtype=torch.int32)
+    with pytest.raises(ValueError, match="v has shape"):
+        c.append(torch.zeros(5, 2, 64), torch.zeros(6, 2, 64), off, pos)
+    assert stub.calls == []
+
+
 def test_binding_refuses_a_cache_of_other_sizes(stub):
     c = pipeline.PagedCache(torch.float32, 4, 16, 2, 64, 2, 3, "cpu")
     off, pos = torch.zeros(3, dtype=torch.int64), torch.zeros(5, dtype=torch.int32)
