@@ -76,8 +76,9 @@ def _uses_debug_hooks(src: str) -> bool:
 
 def build_marshal() -> str | None:
     """The native argument marshalling (csrc/marshal.cpp) for this
-    interpreter; None where there is no C++ compiler or no Python headers (the
-    binding then does the same in Python)."""
+    interpreter; None where there is no C++ compiler, where there are no Python
+    headers, or where the compiler rejects the file (its message is printed, and
+    an older build goes): the binding then does the same in Python."""
     src = os.path.join(CSRC, "marshal.cpp")
     include = sysconfig.get_paths()["include"]
     cxx = shutil.which("g++")
@@ -86,11 +87,16 @@ def build_marshal() -> str | None:
     if (os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src)
             and os.path.getmtime(MARSHAL) >= _newest_header()):
         return MARSHAL
-    tmp = MARSHAL + ".tmp"
+    tmp = f"{MARSHAL}.{os.getpid()}.tmp"  # others may be building too
     r = subprocess.run([cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
                         "-I", include, "-o", tmp, src], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+        sys.stderr.write(f"g++ failed on {src}, the binding stays in Python:\n"
+                         f"{r.stdout}\n{r.stderr}")
+        for path in (tmp, MARSHAL):
+            if os.path.exists(path):
+                os.remove(path)
+        return None
     os.replace(tmp, MARSHAL)
     return MARSHAL
 

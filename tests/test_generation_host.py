@@ -3,6 +3,8 @@ append, tree attention): the oracle against differences and plainer
 restatements, the host refusals of the library and of the binding, and the
 page accounting of PagedCache."""
 
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -271,6 +273,41 @@ def test_attention_refuses_memory_of_other_sizes(stub):
     assert len(stub.calls) == 3
 
 
+def test_a_compiler_that_rejects_the_marshalling_leaves_the_python_path(tmp_path, monkeypatch,
+                                                                        capfd):
+    """build_marshal says so, takes an older build away and goes on; a working
+    compiler's output is put in place whole."""
+    import shutil as sh
+
+    from latent_memory_routing_b200 import build
+
+    so, src = tmp_path / "_marshal.so", tmp_path / "marshal.cpp"
+    include = tmp_path / "include"
+    include.mkdir()
+    (include / "Python.h").touch()
+    src.write_text("not C++")
+    so.write_text("older")
+    os.utime(so, (1, 1))
+    cxx = tmp_path / "g++"
+    monkeypatch.setattr(build, "MARSHAL", str(so))
+    monkeypatch.setattr(build, "CSRC", str(tmp_path))
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(include)})
+    monkeypatch.setattr(sh, "which", lambda name: str(cxx))
+
+    def compiler(script):
+        cxx.write_text("#!/bin/sh\n" + script)
+        cxx.chmod(0o755)
+
+    compiler("echo no such thing >&2\nexit 1\n")
+    assert build.build_marshal() is None
+    assert "no such thing" in capfd.readouterr().err and not so.exists()
+    # the last argument but one is the output
+    compiler('while [ "$1" != -o ]; do shift; done\necho built > "$2"\necho "$2" >&2\nexit 0\n')
+    assert build.build_marshal() == str(so) and so.read_text() == "built\n"
+    assert sorted(p.name for p in tmp_path.iterdir()) == ["_marshal.so", "g++", "include",
+                                                          "marshal.cpp"]
+
+
 # --------------------------------------------------------------- page lists
 
 def test_paged_cache_hands_out_and_takes_back_pages():
@@ -352,7 +389,6 @@ def _flag_overwritten(n_flags, n_sched, items=9, warps=2):
 
 
 def test_tree_attention_flags_outlive_their_readers():
-    import os
     import re
     path = os.path.join(msa.PKG, "csrc", "tree_attn_tc.cu")
     with open(path, encoding="utf-8") as f:
