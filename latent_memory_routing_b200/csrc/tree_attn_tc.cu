@@ -749,12 +749,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                                             fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
             // the reference maximum moves only when a tile exceeds it by 2^8
             const bool grow = row_ok && mt > m_run + kRescaleLog2;
-            float alpha = 1.f;
+            const bool held = m_run != -INFINITY;  // O holds weights, to be scaled
+            float alpha = 1.f;                     // even where alpha underflows to 0
             if (grow) {
               alpha = m_run == -INFINITY ? 0.f : ex2a(m_run - mt);
               m_run = mt;
             }
-            if (t > 0 && __any_sync(0xffffffffu, grow && alpha != 0.f)) {
+            if (t > 0 && __any_sync(0xffffffffu, grow && held)) {
               const uint32_t tO = tmem + 256 + grp * D + lane_addr;
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {

@@ -742,6 +742,81 @@ def test_a_cache_past_32_bit_element_offsets():
     status()
 
 
+# ------------------------------------- long items, to their last slice
+#
+# The bounds of `expected` grow with the keys; these do not.
+
+# dt, page, Hq, H, D, lens, tokens, memory rows, tree, n_max, and a keys' piece
+# of the kernel's (a slice's, or a tenth of a tile's)
+LONG = {
+    "simt-f32": (F32, 16, 2, 1, 64, [1500, 3], [4, 2], [40, 0], "tree", 4, 8),
+    "few-f32": (F32, 64, 8, 4, 128, [32000, 31900, 32050, 7], [1] * 4, [100, 0, 64, 5], "chain",
+                1, 8),
+    "few-f32-trees": (F32, 16, 8, 2, 64, [30011, 0, 8200], [17, 5, 33], [3, 0, 200], "tree", 33,
+                      8),
+    "few-bf16": (BF16, 64, 8, 2, 128, [20000, 4097, 300], [3, 4, 1], [220, 0, 17], "chain", 4, 16),
+    "few-bf16-64": (BF16, 16, 5, 1, 64, [9000, 8999, 1, 0], [3, 1, 2, 3], [], "tree", 3, 16),
+    "tc": (BF16, 64, 8, 2, 128, [18500, 333, 0], [33, 20, 1], [700, 0, 129], "tree", 33, 128),
+    "tc-64": (BF16, 32, 16, 4, 64, [12000, 7000], [60, 33], [0, 31], "pruned", 64, 128),
+    "tc-rows": (BF16, 16, 6, 2, 128, [9001, 15], [64, 9], [], "chain", 64, 128),
+    "tc-two-tiles": (BF16, 128, 8, 2, 128, [80000, 79000, 5], [64, 50, 60], [130, 0, 1], "tree",
+                     64, 128),
+}
+
+
+def long_case(name, seed=5):
+    dt, page, Hq, H, D, lens, toks, mem, tree, n_max, piece = LONG[name]
+    return tree_case(dt, page, Hq, H, D, lens, toks, mem, tree, seed=seed, lead=2), n_max, piece
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_one_key_at_a_border_takes_all_the_weight(name):
+    """Each row looks for a key of its own (a dim that no other key has), the
+    first or last of a slice: the output is that key's value."""
+    t, n_max, _ = long_case(name)
+    c, q, off, parents, km, vm, ml, m_cap = t
+    D, H, G = c.D, c.H, q.shape[1] // c.H
+    o, lens = off.tolist(), c.cache_len.tolist()
+    dead = np.zeros(q.shape[0], dtype=bool)
+    if parents is not None:
+        for b in range(c.B):
+            dead[o[b]:o[b + 1]] = ~oracle.ancestors(parents[o[b]:o[b + 1]].tolist()).diagonal()
+    for turn in range(8):
+        q.zero_()
+        want = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+        for b in range(c.B):
+            n, L, M = o[b + 1] - o[b], lens[b], ml[b].item() if m_cap else 0
+            ends = [j for j in range(M + L) if (j if j < M else j - M) % 8 in (0, 7)]
+            if not ends or n == 0:
+                dead[o[b]:o[b + 1]] = True
+                continue
+            pg, row = rows_of(c, b, range(L))
+            for g in range(H):
+                c.k_pages[pg, g, row] = 0
+                if M:
+                    km[b, :M, g] = 0
+                for r in range(min(n * G, D)):
+                    x = ((r * 8 + turn + g) * 0.6180339887498949) % 1.0
+                    j = ends[int(x * len(ends))]
+                    h = g * G + r % G
+                    q[o[b] + r // G, h, r] = 64
+                    if j < M:
+                        km[b, j, g, r] = 64
+                        want[o[b] + r // G, h] = vm[b, j, g].double()
+                    else:
+                        c.k_pages[pg[j - M], g, row[j - M], r] = 64
+                        want[o[b] + r // G, h] = c.v_pages[pg[j - M], g, row[j - M]].double()
+        # a score of 4096 / D^(1/2) above the others: their weights are 0.  (The
+        # drafted keys keep their random values: 64 of one dim is at most 5 x 64
+        # / D^(1/2), as far below.)
+        out = run_tree(t, n_max).double()
+        seek = (q != 0).any(-1) & torch.from_numpy(~dead).cuda()[:, None]
+        assert int(seek.sum()) > 0
+        diff = (out[seek] - want[seek]).abs()
+        assert bool((diff <= want[seek].abs() * 2.0 ** -20).all()), diff.max()
+    status()
+
+
 # ------------------------------------------------------------- together
 
 def bank(dt, H, D, seed):
