@@ -575,12 +575,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                  fmaxf(mx[6], mx[7]));
         const float mt = mraw * qscale;  // qscale > 0 keeps the order
         const bool grow = mt > m_run + kRescaleLog2;
-        float alpha = 1.f;
+        const bool held = m_run != -INFINITY;  // O holds weights, to be scaled even
+        float alpha = 1.f;                     // where alpha underflows to 0
         if (grow) {
           alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mt);
           m_run = mt;
         }
-        if (__any_sync(0xffffffffu, grow && alpha != 0.f) && j > 0) {
+        if (__any_sync(0xffffffffu, grow && held) && j > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];

@@ -601,6 +601,33 @@ def test_attention_prefill_tensor_core_shapes(B, T, T_loc, Hq, H, D, m_cap, mem_
     status_ok()
 
 
+@pytest.mark.parametrize("dtype,T,T_loc,Hq,H,D,M,tol", [
+    (torch.bfloat16, 300, 300, 8, 2, 128, 200, ATTN_BF16),
+    (torch.bfloat16, 130, 700, 16, 4, 64, 0, ATTN_BF16),
+    (torch.bfloat16, 40, 4000, 4, 1, 128, 300, ATTN_BF16),    # key-tile splits
+    (torch.bfloat16, 1, 900, 8, 2, 128, 500, ATTN_BF16),      # decode
+    (torch.bfloat16, 1, 900, 8, 8, 64, 70, ATTN_BF16),
+    (torch.float32, 9, 500, 4, 2, 64, 30, ATTN_F32),
+])
+def test_attention_a_later_key_far_above_the_others(dtype, T, T_loc, Hq, H, D, M, tol):
+    """Keys of zeros, but one local key in a later tile whose score is 362 or
+    more: the queries behind it take its value, those before it the mean of what
+    they see.  (The one dim that is not zero turns by 1e-4 a position or less.)"""
+    g = torch.Generator(device="cuda").manual_seed(T_loc)
+    q = torch.zeros((1, T, Hq, D), dtype=dtype, device="cuda")
+    q[..., D - 1] = 64
+    km = torch.zeros((1, max(M, 1), H, D), dtype=dtype, device="cuda")
+    kl = torch.zeros((1, T_loc, H, D), dtype=dtype, device="cuda")
+    kl[:, T_loc - T // 2 - 40 if T > 80 else T_loc - 30, :, D - 1] = 64
+    vm, vl = synth.randn(km.shape, dtype, "cuda", g), synth.randn(kl.shape, dtype, "cuda", g)
+    ml = torch.tensor([M], dtype=torch.int32, device="cuda")
+    out = pipeline.Attention(dtype, 1, T, T_loc, Hq, H, D, M, "cuda")(q, km, vm, ml, kl, vl, 16)
+    want = oracle.sparse_attn(f64(q), [f64(km[0, :M])], [f64(vm[0, :M])], f64(kl), f64(vl), 16,
+                              10000.0)
+    assert np.max(np.abs(f64(out) - want)) <= tol * max(1.0, np.max(np.abs(want)))
+    status_ok()
+
+
 @pytest.mark.parametrize("B,T,Hq,H,m_cap,mem_lens", [
     (16, 512, 32, 8, 384, [384] * 8 + [0, 1, 127, 128, 129, 255, 256, 383]),  # ~7 items per CTA
     (2, 64, 32, 8, 3072, [3072, 0]),  # 3 key splits; batch 1's splits past its one tile are empty
