@@ -491,9 +491,11 @@ int msa_qk_norm_rope_backward(msa_dtype dt, msa_dtype grad_dt, int64_t n_tok, in
  *                keys go to the pages, the step's queries (Hq = 0: none) to
  *                q_out in the same launch.
  *   v            [n_tok] tokens of [H][D] (dt), v_stride apart; copied.
- * A page id outside [0, n_pages) or a negative cache length records
- * MSA_ERR_INVALID_ARG in the device status word, a row past the block table
- * MSA_ERR_CAPACITY; that token's K and V are not written.
+ * A row on a page whose id is outside [0, n_pages) or before row 0 (a negative
+ * cache length) records MSA_ERR_INVALID_ARG in the device status word, a row
+ * past the block table MSA_ERR_CAPACITY; the K and V of a token whose row has
+ * no place are not written.  (Of a sequence with a negative length the tokens
+ * from row 0 on have one, among that sequence's own pages.)
  * Supported: page_size in {16,32,64,128}, D in {64,128},
  * n_pages*H*page_size < 2^31. */
 int msa_paged_append(msa_dtype dt, int B, int64_t n_tok, int Hq, int H, int D, const void* q,

@@ -350,6 +350,19 @@ def test_append_skips_rows_it_cannot_place(what, code):
     assert written == 2 + {"page": 1, "minus": 1, "length": 2, "full": 1}[what]
 
 
+def test_a_negative_length_keeps_to_its_own_sequence():
+    """Rows -2 and -1 have no place, rows 0 and 1 do, and the call reports it."""
+    c = paged(3, 2, 64, F32, 16, [16, 16, 16], 5)
+    c.cache_len.copy_(i32([3, -2, 0]))
+    x = rnd((6, 2, 64), F32, 6)
+    c.append(x, x, i64([0, 1, 5, 6]), i32(np.arange(6)))
+    status(-1)
+    want = torch.full_like(c.v_pages, NAN)
+    for b, row, t in ((0, 3, 0), (1, 0, 3), (1, 1, 4), (2, 0, 5)):
+        want[c.block_table[b, 0], :, row] = x[t]
+    assert torch.equal(c.v_pages.view(torch.int32), want.view(torch.int32))
+
+
 @pytest.mark.parametrize("case", ["past_the_reserved", "never_reserved", "released"])
 def test_append_without_a_page_leaves_the_other_sequences_alone(case):
     """The rows of sequence 0, some of them on pages that sequence 1 had."""
