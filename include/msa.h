@@ -529,7 +529,7 @@ int msa_paged_append(msa_dtype dt, int B, int64_t n_tok, int Hq, int H, int D, c
  * included) do not reach its output.  Query head h reads KV head
  * floor(h*H/Hq).  scale <= 0 selects 1/sqrt(D).  Softmax and accumulation in
  * fp32; fp32 operands are not rounded below 2^-20 of a product, and weights
- * that meet bf16 values not below 2^-16 (with up to 16 rows n_max*Hq/H a KV
+ * that meet bf16 values not below 2^-15 (with up to 16 rows n_max*Hq/H a KV
  * head) or 2^-8 (with more).  (In fp32 an
  * infinity among the keys or values that a row does see may make it NaN.)
  * Recorded in the device status word: MSA_ERR_INVALID_ARG for offsets

@@ -5,7 +5,7 @@
 //
 // Mathematics.  As tree_attn_tc.cu: S = Q K^T, p = 2^(scale log2(e) s - m),
 // O += p V, l += p, one pass over the keys.  With bf16 values p is two bf16
-// terms, p = hi + lo to 2^-16 of it: one term alone moved an output by up to
+// terms, p = hi + lo to 2^-15 of it: one term alone moved an output by up to
 // 2^-8 of sum p |v|, more than its own rounding (relative error over an output
 // 0.0023, with two 0.0017), and the second costs 2% (64 sequences x 2,268 keys:
 // 103 us with one, 105 with two).
@@ -127,10 +127,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// What pack2(a, b) = h left of a and b, in bf16 too.
-__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t h) {
-  return pack2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+// Two weights as bf16 terms, hi cut off and the rest rounded.  The rest gets
+// 2^-20 of the weight on top, so that it is 0 only where the weight is: times an
+// infinite value both terms are then that infinity.
+__device__ __forceinline__ uint32_t hi2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
+__device__ __forceinline__ float rest(float a) {
+  return fmaf(a, 1.f + 0x1p-20f, -__uint_as_float(__float_as_uint(a) & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t rest2(float a, float b) { return pack2(rest(a), rest(b)); }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -222,10 +228,10 @@ template <int D> struct Rows<__nv_bfloat16, D> {
   __device__ __forceinline__ static void add(uint32_t vb_u, int lane, const float (&p)[C::NT][4],
                                              float (&o)[D / 8][4]) {
     const int vr = (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
-    const uint32_t pf[4] = {pack2(p[0][0], p[0][1]), pack2(p[0][2], p[0][3]),
-                            pack2(p[1][0], p[1][1]), pack2(p[1][2], p[1][3])};
-    const uint32_t pr[4] = {rest2(p[0][0], p[0][1], pf[0]), rest2(p[0][2], p[0][3], pf[1]),
-                            rest2(p[1][0], p[1][1], pf[2]), rest2(p[1][2], p[1][3], pf[3])};
+    const uint32_t pf[4] = {hi2(p[0][0], p[0][1]), hi2(p[0][2], p[0][3]),
+                            hi2(p[1][0], p[1][1]), hi2(p[1][2], p[1][3])};
+    const uint32_t pr[4] = {rest2(p[0][0], p[0][1]), rest2(p[0][2], p[0][3]),
+                            rest2(p[1][0], p[1][1]), rest2(p[1][2], p[1][3])};
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
       uint32_t b[4];

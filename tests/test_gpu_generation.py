@@ -656,6 +656,39 @@ def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n, rows):
     status()
 
 
+SEEN_INF = {
+    "simt-f32": (F32, 64, [90, 7], [3, 1]),
+    "few-bf16": (BF16, 128, [3000, 7], [3, 1]),
+    "few-bf16-64": (BF16, 64, [90, 0], [1, 1]),
+    "tc": (BF16, 128, [900, 7], [30, 1]),
+    "tc-64": (BF16, 64, [3000, 0], [30, 1]),
+}
+
+
+@pytest.mark.parametrize("name", SEEN_INF)
+def test_an_infinite_value_that_is_seen(name):
+    """In a memory row, a cached row and a sequence's only drafted token: the
+    column becomes that infinity, NaN where two of unlike signs meet, and no
+    other column changes."""
+    dt, D, lens, toks = SEEN_INF[name]
+    t = tree_case(dt, 16, 4, 2, D, lens, toks, [33, 5], "roots", seed=14)
+    c, q, off, parents, km, vm, ml, m_cap = t
+    clean = run_tree(t, max(toks))
+    inf = float("inf")
+    vm[0, 7, 0, 3], vm[1, 4, 1, D - 1] = inf, -inf
+    for b, row, g, d, x in ((0, 11, 0, 40, -inf), (0, lens[0] - 1, 1, 5, inf),
+                            (0, 20, 1, 5, -inf), (1, lens[1], 0, 2, inf),
+                            (1, lens[1], 1, D - 2, -inf)):
+        pg, r = rows_of(c, b, [row])
+        c.v_pages[pg, g, r, d] = x
+    want, n0 = clean.clone(), toks[0]
+    want[:n0, :2, 3], want[:n0, :2, 40], want[:n0, 2:, 5] = inf, -inf, NAN
+    want[n0:, 2:, D - 1], want[n0:, :2, 2], want[n0:, 2:, D - 2] = -inf, inf, -inf
+    assert torch.equal(run_tree(t, max(toks)).nan_to_num(nan=1e9, posinf=2e9, neginf=3e9),
+                       want.nan_to_num(nan=1e9, posinf=2e9, neginf=3e9))
+    status()
+
+
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_scores_of_thousands(dt):
     """Scores of +-thousands: one key takes all the weight, as in the formula."""
