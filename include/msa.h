@@ -530,8 +530,8 @@ int msa_paged_append(msa_dtype dt, int B, int64_t n_tok, int Hq, int H, int D, c
  * floor(h*H/Hq).  scale <= 0 selects 1/sqrt(D).  Softmax and accumulation in
  * fp32; fp32 operands are not rounded below 2^-20 of a product, and weights
  * that meet bf16 values not below 2^-15 (with up to 16 rows n_max*Hq/H a KV
- * head) or 2^-8 (with more).  (In fp32 an
- * infinity among the keys or values that a row does see may make it NaN.)
+ * head) or 2^-8 (with more).  (In fp32 a NaN whose payload lies in its low 13
+ * bits may count as an infinity.)
  * Recorded in the device status word: MSA_ERR_INVALID_ARG for offsets
  * outside [0, n_tok] or falling (the sequence is skipped), more than n_max
  * tokens (only the first n_max are computed), a memory length outside

@@ -170,8 +170,10 @@ __device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint
 }
 // x = hi + lo in tf32 (11 bits each): hi cut off, lo rounded, which leaves
 // 2^-21 of x.  Integer instructions: the conversion's rate is a quarter of
-// theirs (8 x 32,100 keys, 8 / 2 heads, a token: 167 us with it, 143).  A NaN
-// stays one in hi; an infinity becomes inf + (-0).
+// theirs (8 x 32,100 keys, 8 / 2 heads, a token: 167 us with it, 143).  An
+// infinity becomes inf + (-0); a NaN stays one in hi, but for one whose payload
+// lies in the low 13 bits, which becomes an infinity (arithmetic makes no such
+// NaN, and keeping it costs 5%).
 __device__ __forceinline__ uint32_t low32(float x, uint32_t hi) {
   return (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
 }
@@ -179,11 +181,21 @@ __device__ __forceinline__ void split32(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   lo = low32(x, hi);
 }
-// The same, in its place: not taken out of the loop over slices (where 128
-// dims of 16 rows would fill the registers).
-__device__ __forceinline__ void split32_here(float x, uint32_t& hi, uint32_t& lo) {
+// The same of a query's element or a weight, with 2^-23 of it more in lo, about
+// what the product of the rests that is left out amounts to on the average: lo is
+// then 0 only where x is, and both terms times an infinity are that infinity.
+__device__ __forceinline__ uint32_t low32_up(float x, uint32_t hi) {
+  return (__float_as_uint(fmaf(x, 1.f + 0x1p-23f, -__uint_as_float(hi))) + 0x1000u) & 0xffffe000u;
+}
+__device__ __forceinline__ void split32_up(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = low32_up(x, hi);
+}
+// In its place: not taken out of the loop over slices (where 128 dims of 16
+// rows would fill the registers).
+__device__ __forceinline__ void split32_up_here(float x, uint32_t& hi, uint32_t& lo) {
   asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(hi) : "r"(__float_as_uint(x)));
-  lo = low32(x, hi);
+  lo = low32_up(x, hi);
 }
 __device__ __forceinline__ float4 lds128(uint32_t addr) {
   float4 v;
@@ -253,10 +265,9 @@ template <int D> struct Rows<__nv_bfloat16, D> {
 // instead of rounding it, so a slice's P V is summed by itself and added to O by
 // an addition that rounds: O carried through the instructions lost 3e-6 of itself
 // over ranges of 54 slices, more over longer ones (relative error over an output
-// 3.6e-6, so 4.7e-7; 8 sequences x 32,104 keys 141 -> 147 us).  An infinity among the keys or values
-// that a row sees may make it NaN (inf 0).  The order of dims and columns is
-// free, and chosen so that a lane reads 16 bytes at a time without bank
-// conflicts: its dims of a 32-dim block are 8 t .. 8 t + 7, its columns of V
+// 3.6e-6, so 3.5e-7; 8 sequences x 32,104 keys 141 -> 147 us).  The order of dims
+// and columns is free, and chosen so that a lane reads 16 bytes at a time without
+// bank conflicts: its dims of a 32-dim block are 8 t .. 8 t + 7, its columns of V
 // 4 g .. 4 g + 3.
 template <int D> struct Rows<float, D> {
   using C = FC<float, D>;
@@ -293,9 +304,9 @@ template <int D> struct Rows<float, D> {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           if constexpr (D == 128)
-            split32_here(f[x], ah[x], al[x]);
+            split32_up_here(f[x], ah[x], al[x]);
           else
-            split32(f[x], ah[x], al[x]);
+            split32_up(f[x], ah[x], al[x]);
         mma8(s3[0][y], ah, kh[2 * y], kh[2 * y + 1]);
         mma8(s3[1][y], ah, kl[2 * y], kl[2 * y + 1]);
         mma8(s3[2][y], al, kh[2 * y], kh[2 * y + 1]);
@@ -310,10 +321,10 @@ template <int D> struct Rows<float, D> {
                                              float (&o)[D / 8][4]) {
     const int g = lane >> 2, t = lane & 3;
     uint32_t ph[4], pl[4];  // its keys 2 t and 2 t + 1 stand for t and t + 4
-    split32(p[0][0], ph[0], pl[0]);
-    split32(p[0][2], ph[1], pl[1]);
-    split32(p[0][1], ph[2], pl[2]);
-    split32(p[0][3], ph[3], pl[3]);
+    split32_up(p[0][0], ph[0], pl[0]);
+    split32_up(p[0][2], ph[1], pl[1]);
+    split32_up(p[0][1], ph[2], pl[2]);
+    split32_up(p[0][3], ph[3], pl[3]);
 #pragma unroll
     for (int m = 0; m < D / 32; ++m) {
       const uint32_t at = vb_u + m * C::BLK + 2 * t * 128;

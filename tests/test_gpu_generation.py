@@ -658,6 +658,8 @@ def test_unseen_non_finite_values_do_not_reach_a_row(dt, D, n, rows):
 
 SEEN_INF = {
     "simt-f32": (F32, 64, [90, 7], [3, 1]),
+    "few-f32": (F32, 128, [6000, 7], [4, 1]),
+    "few-f32-64": (F32, 64, [9000, 0], [20, 1]),
     "few-bf16": (BF16, 128, [3000, 7], [3, 1]),
     "few-bf16-64": (BF16, 64, [90, 0], [1, 1]),
     "tc": (BF16, 128, [900, 7], [30, 1]),
@@ -686,6 +688,34 @@ def test_an_infinite_value_that_is_seen(name):
     want[n0:, 2:, D - 1], want[n0:, :2, 2], want[n0:, 2:, D - 2] = -inf, inf, -inf
     assert torch.equal(run_tree(t, max(toks)).nan_to_num(nan=1e9, posinf=2e9, neginf=3e9),
                        want.nan_to_num(nan=1e9, posinf=2e9, neginf=3e9))
+    status()
+
+
+@pytest.mark.parametrize("name", SEEN_INF)
+def test_an_infinite_key_that_is_seen(name):
+    """The rows whose score it makes infinite become NaN, those whose score it
+    makes -inf come out as without it, and one without an element there (0 times
+    infinity) is NaN too."""
+    dt, D, lens, toks = SEEN_INF[name]
+    t = tree_case(dt, 16, 4, 2, D, lens, toks, [33, 5], "roots", seed=15)
+    c, q, off, parents, km, vm, ml, m_cap = t
+    n, rows = toks[0], []
+    q[0, 1, 6] = 0                                 # heads 0, 1 read KV head 0
+    q[0, 0, 6], q[0, 2, 9], q[0, 3, 9] = 0.5, -1, -1.3   # few bits: a rest of 0
+    pg, r = rows_of(c, 0, [lens[0] - 1])
+    key = c.k_pages[pg, :, r].clone()
+    c.k_pages[pg, 0, r, 6], c.k_pages[pg, 1, r, 9] = float("inf"), float("inf")
+    out = run_tree(t, max(toks))
+    nan = torch.stack([q[:n, :2, 6] >= 0, q[:n, 2:, 9] >= 0], 1).flatten(1)
+    assert torch.equal(out[:n].isnan(), nan[..., None].expand_as(out[:n]))
+    assert not bool(out[n:].isnan().any()) and bool(nan[0, 0]) and not bool(nan[0, 2])
+    # without it: a key that is far from the query in the same way
+    c.k_pages[pg, :, r] = key
+    c.k_pages[pg, 0, r, 6], c.k_pages[pg, 1, r, 9] = 1e30, 1e30
+    want = exact(t)[:n][~nan]
+    got = out[:n][~nan].double()
+    tol = 2.0 ** -6 if dt == BF16 else 2.0 ** -16
+    assert bool(((got - want).abs() <= tol * want.abs().amax(-1, keepdim=True)).all())
     status()
 
 
