@@ -541,7 +541,10 @@ int msa_paged_append(msa_dtype dt, int B, int64_t n_tok, int Hq, int H, int D, c
  * than the block table holds (rows past it are not seen).
  * Supported: D in {64,128}, Hq % H == 0, Hq/H <= 16, 1 <= n_max <= 128,
  * page_size in {16,32,64,128}, B*H <= 65535.  The workspace size is 0 for
- * unsupported shapes and where none is needed. */
+ * unsupported shapes and where none is needed.  The kernel is chosen by the
+ * lengths that the buffers allow (m_cap, max_pages * page_size), since the
+ * sequences' own are on the device: a table far wider than they need costs
+ * small fp32 calls about 4 us and bf16 trees of more than 192 rows up to 9%. */
 size_t msa_tree_attn_workspace_size(msa_dtype dt, int B, int n_max, int Hq, int H, int D,
                                     int m_cap, int max_pages, int page_size);
 int msa_tree_attn(msa_dtype dt, int B, int64_t n_tok, int n_max, int Hq, int H, int D,

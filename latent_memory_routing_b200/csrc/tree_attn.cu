@@ -329,9 +329,11 @@ int dispatch_simt(const TreeArgs& a, const TreePlan& p, void* ws, cudaStream_t s
 // fp32: once there are 2e7 products of a row and a key's element in the lengths
 // that the buffers allow: its slices and merge take 11 to 14 us at the least,
 // where tree_simt_kernel takes 6 to 9 (2 sequences of 16 tokens over 322 keys,
-// 5e6 products: 12.3 against 9.0; 4 sequences x 4,104 keys, 4 / 16 / 32 rows,
-// 1.7e7 to 1.3e8: 23.6 / 26 / 36 against 23.1 / 28 / 41; 8 x 32,104 keys: 143 /
-// 147 / 273 against 218 / 448 / 742).
+// 2.7e6 products: 12.5 against 8.9; 4 sequences x 4,104 keys, 4 / 16 / 32 rows,
+// 1.7e7 to 1.3e8: 22 / 26 / 34 against 23 / 29 / 42; 8 x 32,104 keys: 147 / 150 /
+// 282 against 218 / 444 / 718).  The lengths themselves are on the device: with
+// a block table 16 times as wide as its sequences need, that first call takes
+// 12.7 us.
 bool takes_few(msa_dtype dt, int B, int n_max, int Hq, int H, int D, int m_cap, int max_pages,
                int page_size) {
   const int rows = n_max * (Hq / H);

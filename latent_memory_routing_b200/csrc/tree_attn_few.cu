@@ -34,11 +34,11 @@
 //     every row) and added at the end for the rows that see them.
 //   * fp32 takes slices of 8 keys on m16n8k8, operands split into two tf32
 //     terms: 96 instructions a slice of 8 KB, which bound it (8 sequences x
-//     32,104 keys: 143 us, 3.7 TB/s; with a third of the products 91 us, 5.8).
+//     32,104 keys: 147 us, 3.6 TB/s; with a third of the products 91 us, 5.8).
 //     More rows are more items over the same keys, side by side and out of the
-//     L2: 64 tokens, 4 sequences x 4,164 keys, 8 / 2 heads, 163 us (27 TFLOP/s;
-//     fp32 register tiles of 64 x 64 one CTA a split took 169, and 648 against
-//     267 for 49 tokens over caches of up to 25,550 rows of unlike lengths).
+//     L2: 64 tokens, 4 sequences x 4,164 keys, 8 / 2 heads, 164 us (27 TFLOP/s;
+//     fp32 register tiles of 64 x 64 one CTA a split took 169, and 2.4 times as
+//     long over caches of unlike lengths up to 25,550 rows).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -477,11 +477,13 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_km,
   }
   const int64_t total = aux.pre[kFewThreads];
   const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x;  // few: on as many SMs
-  // Short items stay whole, a worker each.  Of a long one a range costs its
+  // Short items get a range each, which is an item where their lengths are equal;
+  // of unlike ones the even borders cut most.  Of a long item a range costs its
   // length and the merge their number, so the least length goes with the root
   // of the item's; one slice is too little where that would fill every worker.
-  // (33 sequences of 9 keys: 33 us with ranges of 6 slices at least, 10; one
-  // item of 125 slices: 14 with 6, 10.5; of 1,000: 18 with ranges of one, 14.)
+  // (33 sequences of 9 keys: 33 us with ranges of 6 slices at least, 8; 34 of
+  // unlike lengths up to 175 keys 22; one item of 125 slices: 14 with 6, 12; of
+  // 1,000: 18 with ranges of one, 17.)
   const int64_t all = (int64_t)gridDim.x * kWarps;
   const float mean = (float)total / (float)max(items, (int64_t)1);
   const int64_t least =

@@ -160,7 +160,7 @@ int launch(const TreeArgs& a, int ctas, int per, int part_rows, const float* par
   const int64_t items = std::min<int64_t>(
       workers, (int64_t)a.B * a.H * ((a.n_max * a.G + part_rows - 1) / part_rows));
   // Few items may have many parts each: eight warps then share a row's (two
-  // items of 1,256 slices and 16 rows: 50 us with a warp a row, 20).
+  // items of 1,250 slices and 16 rows: 50 us with a warp a row, 20).
   const bool long_items = items * 32 <= workers;
   const int most = long_items ? 2 : kMergeWarps;
   const int y = (2 * num_sms() + chunks - 1) / chunks * (long_items ? 3 : 1);
@@ -169,7 +169,8 @@ int launch(const TreeArgs& a, int ctas, int per, int part_rows, const float* par
                       part_rows, part_o, part_ml, cuts);
   };
   // Few rows: one block an SM, with more loads in flight (one sequence of 4,316
-  // keys: 13.4 us, 15.3 with two); many: two blocks (16 trees of 48: 158, 166).
+  // keys: 13.8 us, 14.8 with two); many: two blocks (16 trees of up to 48 tokens:
+  // 103, with one 110).
   return items * part_rows <= 2LL * kMergeWarps * num_sms() ? go(tree_merge_kernel<T, D, 1>)
                                                             : go(tree_merge_kernel<T, D, 2>);
 }

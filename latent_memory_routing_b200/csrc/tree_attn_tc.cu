@@ -18,17 +18,19 @@
 // cores and the exponentials.  So the same tile shape serves all R: rows
 // padded to the MMA's M = 128 cost tensor time that the stream hides.
 // Measured (32 / 8 heads x 128): 16 sequences x 8,220 keys, 9 to 32 tokens
-// each, 103 to 116 us (5.3 to 4.7 TB/s); 2 x 150,001 keys, 64 tokens, 320 to
-// 375 us as the clock goes (0.84 to 0.98 PFLOP/s: the chain softmax -> P V -> S
-// of each stream, 3,650 cycles a tile of which the tensor pipe works 2,048).
+// each, 102 to 111 us (5.3 to 4.9 TB/s); 2 x 150,065 keys, 64 tokens, 312 us at
+// 1,965 MHz and 378 under the power cap at 1,460 (1.01 to 0.83 PFLOP/s: the chain
+// softmax -> P V -> S of each stream, 3,650 cycles a tile of which the tensor pipe
+// works 2,048).
 //
 // Design.
 //   * Even work: the 128-key tiles of all (sequence, KV head, row block)
 //     items in one line, each item's behind kItemCost units that stand for its
 //     start and end (without them a CTA of short items ended at 248,000
-//     cycles, the others at 145,000; 16 sequences x 8,220 keys, up to 48
-//     tokens: 124 us with 1, 108 with 3, 103 with 5, 102 with 8), cut into one
-//     contiguous range a CTA (one CTA an SM).
+//     cycles, the others at 145,000; 16 sequences of unlike lengths up to 8,220
+//     keys, up to 48 tokens: 128 us with 1, 108 with 3, 103 with 5, 104 with 8;
+//     64 sequences x 164 keys, 64 tokens: 81, 78, 78, 74), cut into one contiguous
+//     range a CTA (one CTA an SM).
 //     An item inside one range is written directly; an item cut by a range
 //     border is written as fp32 partials (at most two a CTA) that a second
 //     launch merges in a fixed order.  The lengths stay on the device: every
@@ -38,10 +40,12 @@
 //     thread a row).  Up to 128 rows (kQT = 1) the streams take the key tiles
 //     in turn and join their (m, l, O) at an item's end, so a stream has the
 //     time of two tiles; with kQT = 2 each holds 128 of an item's 256 rows and
-//     both read the same tile.  More than 128 rows are items of their own over
-//     the same keys, out of the L2 (16 sequences x 8,220 keys, 33 tokens: 75 us
-//     against 92 with kQT = 2), until the L2 cannot hold what two
-//     of them share (see tc_plan).
+//     both read the same tile.  129 to 192 rows, and more where the L2 holds
+//     what two of them share (see tc_plan), are items of their own over the same
+//     keys: 16 sequences of unlike lengths up to 8,253 keys, 33 tokens (304 MB),
+//     76 us against 91 with kQT = 2, whose longest items end late.  (Of equal
+//     lengths it is the other way round: 16 x 8,220 keys, 33 / 48 tokens, 187 / 192
+//     us against 146 / 157.)
 //   * Warp 0 loads K tiles, warp 3 V tiles (rings of their own: a K slot is
 //     free after S, a V slot after P V), one lane a page (or 32 memory rows):
 //     only pages that hold rows are read.  Warp 2 walks the range, publishes
@@ -958,8 +962,11 @@ struct TcPlan {
 // rows (fewer leave much of the second tile empty, and its time is spent all
 // the same) of 128 dims (at 64 the chain of a tile, not HBM, is the bound), and
 // more keys and values in the lengths that the buffers allow than the L2 keeps:
-// 64 tokens, 2 sequences x 20,064 keys (164 MB) 65 us against 71 with kQT = 1,
-// x 150,065 311 against 380; 16 x 2,064 (135 MB) 84 against 79.
+// 64 tokens, 2 sequences x 20,064 keys (164 MB) 61 us against 72 with kQT = 1,
+// x 150,065 311 against 383; 4 x 564 (9 MB) 26.7 against 24.3.  In between the two
+// are even (16 x 1,064 and 16 x 2,064, 70 and 135 MB: 60 to 66 and 76 to 88 us
+// either way, as the GPU goes).  The lengths themselves are on the device: with a
+// block table 16 times as wide as its sequences need, 4 x 564 keys take 26.5 us.
 // The Q buffers hold no more rows than a tile can have (the MMA reads on into
 // the ring: rows of S that nobody reads).
 TcPlan tc_plan(int B, int n_max, int G, int H, int D, int64_t keys) {
